@@ -14,7 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import numpy as np
 import torch
@@ -40,6 +40,12 @@ EP_SCALE_ROUND = 1 << 5
 EP_SCALE_MN_MAJOR = 1 << 6
 EP_CONSUME_SIGNAL_DONE = 1 << 7
 EP_CONSUME_STAMPS = 1 << 8
+
+EP_GRAD_F32 = 1 << 9
+EP_GRAD_ACCUMULATE = 1 << 10
+
+# activations of the experts' feed-forward by name
+ACTIVATIONS = {"silu": 0, "gelu": 1}
 
 # scale flavours by name: flags, element dtype
 SCALE_KINDS = {
@@ -70,6 +76,7 @@ EXPORTS = [
     "ep_tile_consume", "ep_status_string", "ep_borrow_release", "ep_combine_backward",
     "ep_dispatch_backward", "ep_combine_gated", "ep_fp8_cast_back", "ep_scale_ld",
     "ep_layout_noalloc", "ep_set_density_hint", "ep_layout_density", "ep_layout_dispatch",
+    "ep_expert_ffn", "ep_expert_ffn_backward",
 ]
 
 EP_DENSITY_AUTO = 0
@@ -120,6 +127,8 @@ def _load() -> ctypes.CDLL:
         "ep_fp8_cast_back": (st, [P, P, U32, I64, I64, I32, P, P]),
         "ep_scale_ld": (I64, [P]),
         "ep_layout_noalloc": (st, [P, I32, I32, I32, I32, I64, P, P, P, P, P, P, P, P, P]),
+        "ep_expert_ffn": (st, [P, U32, P, I32, P, P, I32, I32, P, P, P, P]),
+        "ep_expert_ffn_backward": (st, [P, U32, P, P, I32, P, P, I32, I32, P, P, U32, P, P, P, P, P]),
         "ep_set_density_hint": (st, [P, I32]),
         "ep_layout_density": (I32, [P, P]),
     }
@@ -144,6 +153,15 @@ def _ptr(t: Optional[torch.Tensor]):
 def _stream(stream) -> ctypes.c_void_p:
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _used_on(stream, *tensors) -> None:
+    """Tensors made here for a call on another stream than the current one: their
+    memory is not handed out again before that stream is past the call."""
+    if stream is not None and stream != torch.cuda.current_stream():
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
 
 
 def _check(status: int, where: str):
@@ -279,6 +297,26 @@ def ep_dispatch_backward(h, epoch: int, grad_pool: torch.Tensor, grad_x: torch.T
                                      _stream(stream)), "ep_dispatch_backward")
 
 
+def ep_expert_ffn(h, epoch: int, pool: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor,
+                  activation: int, act: torch.Tensor, gate_up: Optional[torch.Tensor], out: torch.Tensor,
+                  stream=None) -> None:
+    _check(_lib.ep_expert_ffn(h, epoch, _ptr(pool), pool.shape[1], _ptr(w_gate_up), _ptr(w_down),
+                              w_down.shape[2], activation, _ptr(act), _ptr(gate_up), _ptr(out),
+                              _stream(stream)), "ep_expert_ffn")
+
+
+def ep_expert_ffn_backward(h, epoch: int, grad_out: torch.Tensor, pool: torch.Tensor,
+                           w_gate_up: torch.Tensor, w_down: torch.Tensor, activation: int,
+                           act: torch.Tensor, gate_up: torch.Tensor, flags: int,
+                           grad_gate_up: torch.Tensor, grad_pool: Optional[torch.Tensor],
+                           grad_w_gate_up: Optional[torch.Tensor], grad_w_down: Optional[torch.Tensor],
+                           stream=None) -> None:
+    _check(_lib.ep_expert_ffn_backward(h, epoch, _ptr(grad_out), _ptr(pool), pool.shape[1], _ptr(w_gate_up),
+                                       _ptr(w_down), w_down.shape[2], activation, _ptr(act), _ptr(gate_up),
+                                       flags, _ptr(grad_gate_up), _ptr(grad_pool), _ptr(grad_w_gate_up),
+                                       _ptr(grad_w_down), _stream(stream)), "ep_expert_ffn_backward")
+
+
 def ep_borrow_release(h, consumer_stream=None) -> None:
     _check(_lib.ep_borrow_release(h, _stream(consumer_stream)), "ep_borrow_release")
 
@@ -288,6 +326,12 @@ def ep_handle_sync_status(h, stream=None) -> int:
 
 
 # ------------------------------------------------------------- convenience --
+
+class FfnSaved(NamedTuple):
+    """What expert_ffn(save=True) keeps for expert_ffn_backward."""
+    act: torch.Tensor           # bf16 [capacity_rows, inter]
+    gate_up: torch.Tensor       # fp32 [capacity_rows, 2 * inter]
+
 
 class EpHandle:
     """One layout's metadata on the current device (owns an ep_handle)."""
@@ -417,6 +461,103 @@ class EpHandle:
             raise ValueError("grad_x must be [num_tokens, H]")
         ep_dispatch_backward(self._h, epoch, grad_pool, grad_x, stream)
         return grad_x
+
+    def _check_rows(self, t: torch.Tensor, width: int, dtype, name: str) -> None:
+        _require(t, dtype, name, self.device)
+        if t.dim() != 2 or t.shape[0] < self.capacity_rows or t.shape[1] != width:
+            raise ValueError(f"{name} must be at least [{self.capacity_rows}, {width}]")
+
+    def _check_experts(self, pool: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor,
+                       activation: str) -> Tuple[int, int]:
+        """(hidden, inter) of a feed-forward's operands."""
+        if activation not in ACTIVATIONS:
+            raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
+        _require(w_gate_up, torch.bfloat16, "w_gate_up", self.device)
+        _require(w_down, torch.bfloat16, "w_down", self.device)
+        E = self.num_experts
+        if w_down.dim() != 3 or w_down.shape[0] != E:
+            raise ValueError(f"w_down must be [{E}, hidden, inter]")
+        H, I = int(w_down.shape[1]), int(w_down.shape[2])
+        if tuple(w_gate_up.shape) != (E, 2 * I, H):
+            raise ValueError(f"w_gate_up must be [{E}, {2 * I}, {H}]")
+        self._check_rows(pool, H, torch.bfloat16, "pool")
+        return H, I
+
+    def expert_ffn(self, epoch: int, pool: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor,
+                   activation: str = "silu", out: Optional[torch.Tensor] = None,
+                   act: Optional[torch.Tensor] = None, gate_up: Optional[torch.Tensor] = None,
+                   save: bool = False, stream=None):
+        """The experts' gated feed-forward over the dispatched pool:
+        out = (act(x Wg^T) * (x Wu^T)) Wd^T per real row, bf16
+        [capacity_rows, hidden], combine()'s expert_out.
+
+        w_gate_up is [num_experts, 2 * inter, hidden] (gate rows, then up rows),
+        w_down [num_experts, hidden, inter], both bf16.  With save=True returns
+        (out, FfnSaved) for expert_ffn_backward; act and gate_up are the buffers
+        to use for it (made when not given; act also without save, as the
+        call's workspace)."""
+        H, I = self._check_experts(pool, w_gate_up, w_down, activation)
+        cap = self.capacity_rows
+        if gate_up is not None and not save:
+            raise ValueError("gate_up is written with save=True only")
+        if out is None:
+            out = torch.empty(cap, H, dtype=torch.bfloat16, device=self.device)
+        if act is None:
+            act = torch.empty(cap, I, dtype=torch.bfloat16, device=self.device)
+        if save and gate_up is None:
+            gate_up = torch.empty(cap, 2 * I, dtype=torch.float32, device=self.device)
+        self._check_rows(out, H, torch.bfloat16, "out")
+        self._check_rows(act, I, torch.bfloat16, "act")
+        if save:
+            self._check_rows(gate_up, 2 * I, torch.float32, "gate_up")
+        ep_expert_ffn(self._h, epoch, pool, w_gate_up, w_down, ACTIVATIONS[activation], act, gate_up, out, stream)
+        _used_on(stream, out, act, gate_up)
+        return (out, FfnSaved(act, gate_up)) if save else out
+
+    def expert_ffn_backward(self, epoch: int, grad_out: torch.Tensor, pool: torch.Tensor,
+                            w_gate_up: torch.Tensor, w_down: torch.Tensor, saved: FfnSaved,
+                            activation: str = "silu", grad_pool: Optional[torch.Tensor] = None,
+                            grad_w_gate_up: Optional[torch.Tensor] = None,
+                            grad_w_down: Optional[torch.Tensor] = None, accumulate: bool = False,
+                            grad_gate_up: Optional[torch.Tensor] = None, stream=None):
+        """Backward of expert_ffn: returns (grad_pool, grad_w_gate_up,
+        grad_w_down) for grad_out, combine_backward()'s grad_expert_out.
+
+        The weight gradients are bf16 or float32, as the buffers given (bf16
+        when none is); accumulate=True adds to float32 buffers.  grad_gate_up
+        is the workspace, bf16 [capacity_rows, 2 * inter] (made when not given)."""
+        H, I = self._check_experts(pool, w_gate_up, w_down, activation)
+        E = self.num_experts
+        self._check_rows(grad_out, H, torch.bfloat16, "grad_out")
+        self._check_rows(saved.act, I, torch.bfloat16, "saved.act")
+        self._check_rows(saved.gate_up, 2 * I, torch.float32, "saved.gate_up")
+        given = [g for g in (grad_w_gate_up, grad_w_down) if g is not None]
+        dtype = given[0].dtype if given else torch.bfloat16
+        if dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError(f"weight gradients must be bfloat16 or float32, got {dtype}")
+        if accumulate and (len(given) < 2 or dtype != torch.float32):
+            raise ValueError("accumulate needs both weight gradients, in float32")
+        if grad_pool is None:
+            grad_pool = torch.empty(self.capacity_rows, H, dtype=torch.bfloat16, device=self.device)
+        if grad_w_gate_up is None:
+            grad_w_gate_up = torch.empty(E, 2 * I, H, dtype=dtype, device=self.device)
+        if grad_w_down is None:
+            grad_w_down = torch.empty(E, H, I, dtype=dtype, device=self.device)
+        if grad_gate_up is None:
+            grad_gate_up = torch.empty(self.capacity_rows, 2 * I, dtype=torch.bfloat16, device=self.device)
+        self._check_rows(grad_pool, H, torch.bfloat16, "grad_pool")
+        self._check_rows(grad_gate_up, 2 * I, torch.bfloat16, "grad_gate_up")
+        for g, shape, name in ((grad_w_gate_up, (E, 2 * I, H), "grad_w_gate_up"),
+                               (grad_w_down, (E, H, I), "grad_w_down")):
+            _require(g, dtype, name, self.device)
+            if tuple(g.shape) != shape:
+                raise ValueError(f"{name} must be {list(shape)}")
+        flags = (EP_GRAD_F32 if dtype == torch.float32 else 0) | (EP_GRAD_ACCUMULATE if accumulate else 0)
+        ep_expert_ffn_backward(self._h, epoch, grad_out, pool, w_gate_up, w_down, ACTIVATIONS[activation],
+                               saved.act, saved.gate_up, flags, grad_gate_up, grad_pool, grad_w_gate_up,
+                               grad_w_down, stream)
+        _used_on(stream, grad_pool, grad_gate_up, grad_w_gate_up, grad_w_down)
+        return grad_pool, grad_w_gate_up, grad_w_down
 
     def borrow(self, x: torch.Tensor, stream=None) -> int:
         """Dispatch without a copy: lend x through the row map

@@ -343,6 +343,63 @@ ep_status ep_combine_backward(const ep_handle* h, uint32_t epoch, const void* gr
 ep_status ep_dispatch_backward(const ep_handle* h, uint32_t epoch, const void* grad_pool,
                                int32_t hidden, void* grad_x, hipStream_t stream);
 
+/* The experts' gated feed-forward, between ep_dispatch and ep_combine: for
+ * each real pool row x of expert e, with act the activation,
+ *     g = x Wg[e]^T, u = x Wu[e]^T, a = act(g) * u, out = a Wd[e]^T.
+ *   epoch       the layout's epoch, else EP_ERR_HANDLE_STATE.
+ *   pool        device bf16 [capacity_rows, hidden] (the bf16 dispatch's pool;
+ *               of an FP8 pool, its ep_fp8_cast_back).
+ *   w_gate_up   device bf16 [num_experts, 2 * inter, hidden]: an expert's
+ *               inter gate rows, then its inter up rows.
+ *   w_down      device bf16 [num_experts, hidden, inter].
+ *   activation  EP_ACT_SILU: g / (1 + exp(-g)); EP_ACT_GELU: the tanh form,
+ *               g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))).
+ *   act         device bf16 [capacity_rows, inter]: receives a (the call's
+ *               workspace, and an input of the backward pass).
+ *   gate_up     device fp32 [capacity_rows, 2 * inter], or NULL: receives g and
+ *               u for the backward pass.
+ *   out         device bf16 [capacity_rows, hidden] (ep_combine's expert_out);
+ *               may be the pool itself, otherwise no buffer that is written
+ *               may share memory with another (EP_ERR_INVALID_ARGUMENT).
+ * hidden % 8 == 0, inter % 8 == 0; hidden * inter above 2^29, or either above
+ * 65536, is EP_ERR_UNSUPPORTED.  Sums are fp32; a and out are each rounded
+ * once, to nearest even.  Only real rows are read and written: rows past an
+ * expert's last keep what they hold, in every buffer.  The result depends on
+ * the rows alone, never on timing.  Two launches; capturable. */
+#define EP_ACT_SILU 0
+#define EP_ACT_GELU 1
+ep_status ep_expert_ffn(const ep_handle* h, uint32_t epoch, const void* pool, int32_t hidden,
+                        const void* w_gate_up, const void* w_down, int32_t inter, int32_t activation,
+                        void* act, float* gate_up, void* out, hipStream_t stream);
+
+/* Backward of ep_expert_ffn, between ep_combine_backward (whose
+ * grad_expert_out is grad_out here) and ep_dispatch_backward (whose grad_pool
+ * this writes).  With da = grad_out Wd:
+ *     dg = da * u * act'(g), du = da * act(g),
+ *     grad_pool = dg Wg + du Wu,
+ *     grad_Wg = dg^T x, grad_Wu = du^T x, grad_Wd = grad_out^T a,
+ * the last three summed over the real rows of each expert.
+ *   pool, w_*, inter, activation   as in the forward call.
+ *   act, gate_up    what the forward call wrote for this layout.
+ *   flags           EP_GRAD_F32: the weight gradients are fp32, else bf16;
+ *                   EP_GRAD_ACCUMULATE: they are added to what the buffers
+ *                   hold (with EP_GRAD_F32 only, else EP_ERR_UNSUPPORTED).
+ *   grad_gate_up    device bf16 [capacity_rows, 2 * inter]: receives dg and du.
+ *   grad_pool       device bf16 [capacity_rows, hidden], or NULL to leave out.
+ *   grad_w_gate_up  device [num_experts, 2 * inter, hidden], or NULL.
+ *   grad_w_down     device [num_experts, hidden, inter], or NULL.
+ * An expert without rows gets zero weight gradients (or keeps its sums).
+ * Sums are fp32 in a fixed order (no atomics); dg, du and bf16 results are
+ * rounded once.  Buffers that are written must not share memory with any
+ * other.  Up to four launches; capturable. */
+#define EP_GRAD_F32        (1u << 9)
+#define EP_GRAD_ACCUMULATE (1u << 10)
+ep_status ep_expert_ffn_backward(const ep_handle* h, uint32_t epoch, const void* grad_out, const void* pool,
+                                 int32_t hidden, const void* w_gate_up, const void* w_down, int32_t inter,
+                                 int32_t activation, const void* act, const float* gate_up, uint32_t flags,
+                                 void* grad_gate_up, void* grad_pool, void* grad_w_gate_up,
+                                 void* grad_w_down, hipStream_t stream);
+
 /* End the lease of a borrowing dispatch ([BORROW]).  consumer_stream is the
  * stream the consumers of the view were enqueued on; the handle's next call
  * waits (on its own stream) until that stream's work enqueued so far is done,
