@@ -13,6 +13,7 @@ ep_layout, ep_dispatch, ep_combine, ...); ``EpHandle`` bundles them.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 from typing import NamedTuple, Optional, Tuple
 
@@ -43,6 +44,16 @@ EP_CONSUME_STAMPS = 1 << 8
 
 EP_GRAD_F32 = 1 << 9
 EP_GRAD_ACCUMULATE = 1 << 10
+
+EP_ROUTE_BF16 = 1 << 11
+EP_ROUTE_SIGMOID = 1 << 12
+EP_ROUTE_NORMALIZE = 1 << 13
+EP_ADAMW_PARAM_BF16 = 1 << 14
+EP_ADAMW_GRAD_BF16 = 1 << 15
+EP_ADAMW_STATE_8BIT = 1 << 16
+
+# scores of the router by name: flags
+SCORES = {"softmax": 0, "sigmoid": EP_ROUTE_SIGMOID}
 
 # activations of the experts' feed-forward by name
 ACTIVATIONS = {"silu": 0, "gelu": 1}
@@ -76,7 +87,7 @@ EXPORTS = [
     "ep_tile_consume", "ep_status_string", "ep_borrow_release", "ep_combine_backward",
     "ep_dispatch_backward", "ep_combine_gated", "ep_fp8_cast_back", "ep_scale_ld",
     "ep_layout_noalloc", "ep_set_density_hint", "ep_layout_density", "ep_layout_dispatch",
-    "ep_expert_ffn", "ep_expert_ffn_backward",
+    "ep_expert_ffn", "ep_expert_ffn_backward", "ep_route", "ep_route_backward", "ep_adamw",
 ]
 
 EP_DENSITY_AUTO = 0
@@ -93,6 +104,18 @@ class EpError(RuntimeError):
 class _Config(ctypes.Structure):
     _fields_ = [("max_tokens", ctypes.c_int32), ("top_k", ctypes.c_int32),
                 ("num_experts", ctypes.c_int32), ("block_m", ctypes.c_int32)]
+
+
+class _AdamwConfig(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64),
+                ("step_dev", ctypes.c_void_p), ("grad_scale_dev", ctypes.c_void_p),
+                ("grad_scale", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
+# ep_adamw_tensor, one row of an array
+_ADAMW_TENSOR = np.dtype([(k, np.uint64) for k in ("param", "grad", "exp_avg", "exp_avg_sq", "exp_avg_scale",
+                                                   "exp_avg_sq_scale", "copy")] + [("n", np.int64)])
 
 
 def _load() -> ctypes.CDLL:
@@ -129,6 +152,9 @@ def _load() -> ctypes.CDLL:
         "ep_layout_noalloc": (st, [P, I32, I32, I32, I32, I64, P, P, P, P, P, P, P, P, P]),
         "ep_expert_ffn": (st, [P, U32, P, I32, P, P, I32, I32, P, P, P, P]),
         "ep_expert_ffn_backward": (st, [P, U32, P, P, I32, P, P, I32, I32, P, P, U32, P, P, P, P, P]),
+        "ep_route": (st, [P, I64, I32, I32, I32, U32, P, ctypes.c_float, P, P, P]),
+        "ep_route_backward": (st, [P, I64, I32, I32, I32, U32, ctypes.c_float, P, P, P, I64, P]),
+        "ep_adamw": (st, [P, I32, ctypes.POINTER(_AdamwConfig), P]),
         "ep_set_density_hint": (st, [P, I32]),
         "ep_layout_density": (I32, [P, P]),
     }
@@ -323,6 +349,151 @@ def ep_borrow_release(h, consumer_stream=None) -> None:
 
 def ep_handle_sync_status(h, stream=None) -> int:
     return int(_lib.ep_handle_sync_status(h, _stream(stream)))
+
+
+def _route_args(logits: torch.Tensor, score: str, normalize: bool) -> int:
+    """Checks a router's logits; returns the call's flags."""
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {sorted(SCORES)}")
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    if not logits.is_cuda:
+        raise ValueError(f"logits must be on a GPU, got {logits.device}")
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1) or _row_stride(logits) < logits.shape[1]:
+        raise ValueError("logits must be [num_tokens, num_experts] with contiguous rows that do not overlap")
+    return SCORES[score] | (EP_ROUTE_NORMALIZE if normalize else 0) | \
+        (EP_ROUTE_BF16 if logits.dtype == torch.bfloat16 else 0)
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: Optional[torch.Tensor] = None,
+          normalize: bool = True, scale: float = 1.0, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The router: (topk_idx int32, topk_weights fp32), both [num_tokens, top_k],
+    from logits [num_tokens, num_experts] (fp32 or bf16, rows may be strided).
+
+    score "softmax" or "sigmoid"; bias [num_experts] is added to sigmoid scores
+    for the choice alone; normalize divides a token's weights by their sum.
+    Equal scores: the lowest expert first.  -inf closes an expert; slots without
+    an expert get -1 and weight 0 (masked for layout())."""
+    flags = _route_args(logits, score, normalize)
+    T, E = logits.shape
+    if bias is not None:
+        _require(bias, torch.float32, "bias", logits.device)
+        if tuple(bias.shape) != (E,):
+            raise ValueError(f"bias must be [{E}]")
+    with torch.cuda.device(logits.device):
+        idx = torch.empty(T, top_k, dtype=torch.int32, device=logits.device)
+        w = torch.empty(T, top_k, dtype=torch.float32, device=logits.device)
+        _check(_lib.ep_route(_ptr(logits), _row_stride(logits), T, E, top_k, flags, _ptr(bias), scale, _ptr(idx),
+                             _ptr(w), _stream(stream)), "ep_route")
+        _used_on(stream, idx, w)
+    return idx, w
+
+
+def route_backward(logits: torch.Tensor, topk_idx: torch.Tensor, grad_weights: torch.Tensor,
+                   score: str = "softmax", normalize: bool = True, scale: float = 1.0,
+                   grad_logits: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Backward of route: the logits' gradient, in their type, from that of the
+    weights (combine_backward()'s grad_weights)."""
+    flags = _route_args(logits, score, normalize)
+    T, E = logits.shape
+    _require(topk_idx, torch.int32, "topk_idx", logits.device)
+    _require(grad_weights, torch.float32, "grad_weights", logits.device)
+    if topk_idx.dim() != 2 or topk_idx.shape[0] != T or grad_weights.shape != topk_idx.shape:
+        raise ValueError("topk_idx / grad_weights must both be [num_tokens, top_k]")
+    with torch.cuda.device(logits.device):
+        if grad_logits is None:
+            grad_logits = torch.empty(T, E, dtype=logits.dtype, device=logits.device)
+        if grad_logits.dtype != logits.dtype or grad_logits.device != logits.device or \
+                grad_logits.shape != logits.shape or (E > 1 and grad_logits.stride(1) != 1) or \
+                _row_stride(grad_logits) < E:
+            raise ValueError("grad_logits must be like logits")
+        _check(_lib.ep_route_backward(_ptr(logits), _row_stride(logits), T, E, topk_idx.shape[1], flags, scale,
+                                      _ptr(topk_idx), _ptr(grad_weights), _ptr(grad_logits),
+                                      _row_stride(grad_logits), _stream(stream)), "ep_route_backward")
+        _used_on(stream, grad_logits)
+    return grad_logits
+
+
+_attr = operator.attrgetter
+
+
+def _column(tensors, dtype, sizes, device, name: str):
+    """Addresses of one kind of the step's tensors, checked.  A model has
+    hundreds: each check is one pass of a C function over the list."""
+    if len(tensors) != len(sizes):
+        raise ValueError(f"{name} must have {len(sizes)} tensors, got {len(tensors)}")
+    if list(map(torch.Tensor.numel, tensors)) != sizes:
+        raise ValueError(f"{name}: a tensor has another number of values than its parameter needs")
+    for key, want in ((_attr("dtype"), dtype), (_attr("device"), device), (torch.Tensor.is_contiguous, True)):
+        got = set(map(key, tensors))
+        if got != {want}:
+            what = "contiguous" if want is True else want
+            raise (TypeError if want is dtype else ValueError)(f"{name} must be {what}, got {got - {want}}")
+    return list(map(torch.Tensor.data_ptr, tensors))
+
+
+def adamw(params, grads, exp_avgs, exp_avg_sqs, step, lr: float = 1e-3, beta1: float = 0.9, beta2: float = 0.999,
+          eps: float = 1e-8, weight_decay: float = 1e-2, exp_avg_scales=None, exp_avg_sq_scales=None, copies=None,
+          grad_scale=1.0, stream=None) -> None:
+    """One AdamW step over lists of tensors, in place.
+
+    params float32 or bfloat16, grads float32 or bfloat16 (each list of one
+    type); exp_avgs and exp_avg_sqs float32, or uint8 with exp_avg_scales and
+    exp_avg_sq_scales (float32, one for each 128 values): e4m3fn codes of the
+    first moment and of the root of the second, which cast_back's "f32" flavour
+    reads.  copies: bfloat16 tensors that receive the updated float32
+    parameters.  step: the step's number from 1, or an int64 tensor on the GPU
+    that holds it when the step runs (for graphs); grad_scale: a number or a
+    float32 tensor on the GPU that the gradients are multiplied by."""
+    n = len(params)
+    if n == 0:
+        return
+    device, eight = params[0].device, exp_avg_scales is not None
+    if eight != (exp_avg_sq_scales is not None):
+        raise ValueError("8-bit states need exp_avg_scales and exp_avg_sq_scales")
+    if device.type != "cuda":
+        raise ValueError(f"params must be on a GPU, got {device}")
+    p_dtype, g_dtype = params[0].dtype, grads[0].dtype if len(grads) else None
+    for dtype, name in ((p_dtype, "params"), (g_dtype, "grads")):
+        if dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"{name} must be float32 or bfloat16, got {dtype}")
+    sizes = list(map(torch.Tensor.numel, params))
+    state = torch.uint8 if eight else torch.float32
+    t = np.zeros(n, _ADAMW_TENSOR)
+    t["n"] = sizes
+    t["param"] = _column(params, p_dtype, sizes, device, "params")
+    t["grad"] = _column(grads, g_dtype, sizes, device, "grads")
+    t["exp_avg"] = _column(exp_avgs, state, sizes, device, "exp_avgs")
+    t["exp_avg_sq"] = _column(exp_avg_sqs, state, sizes, device, "exp_avg_sqs")
+    if eight:
+        blocks = [(k + 127) // 128 for k in sizes]
+        t["exp_avg_scale"] = _column(exp_avg_scales, torch.float32, blocks, device, "exp_avg_scales")
+        t["exp_avg_sq_scale"] = _column(exp_avg_sq_scales, torch.float32, blocks, device, "exp_avg_sq_scales")
+    if copies is not None:
+        t["copy"] = _column(copies, torch.bfloat16, sizes, device, "copies")
+    cfg = _AdamwConfig(lr=lr, beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay, grad_scale=1.0)
+    cfg.flags = (EP_ADAMW_PARAM_BF16 if p_dtype == torch.bfloat16 else 0) | \
+        (EP_ADAMW_GRAD_BF16 if g_dtype == torch.bfloat16 else 0) | (EP_ADAMW_STATE_8BIT if eight else 0)
+    if isinstance(step, torch.Tensor):
+        _require(step, torch.int64, "step", device)
+        if step.numel() != 1:
+            raise ValueError("step must hold one number")
+        cfg.step_dev = step.data_ptr()
+    else:
+        cfg.step = int(step)
+    if isinstance(grad_scale, torch.Tensor):
+        _require(grad_scale, torch.float32, "grad_scale", device)
+        if grad_scale.numel() != 1:
+            raise ValueError("grad_scale must hold one number")
+        cfg.grad_scale_dev = grad_scale.data_ptr()
+    else:
+        cfg.grad_scale = float(grad_scale)
+    with torch.cuda.device(device):
+        _check(_lib.ep_adamw(t.ctypes.data_as(ctypes.c_void_p), n, ctypes.byref(cfg), _stream(stream)), "ep_adamw")
 
 
 # ------------------------------------------------------------- convenience --

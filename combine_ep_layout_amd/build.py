@@ -17,7 +17,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libep_layout.so")
 SOURCES = [os.path.join(CSRC, "ep_kernels.hip"), os.path.join(CSRC, "ep_api.hip"),
-           os.path.join(CSRC, "ep_noalloc.hip"), os.path.join(CSRC, "ep_ffn.hip")]
+           os.path.join(CSRC, "ep_noalloc.hip"), os.path.join(CSRC, "ep_ffn.hip"),
+           os.path.join(CSRC, "ep_route.hip"), os.path.join(CSRC, "ep_adamw.hip")]
 CEILING_LIB = os.path.join(PKG, "libep_ceiling.so")
 CEILING_SOURCES = [os.path.join(CSRC, "ep_ceiling.hip")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -170,6 +170,43 @@ int32_t ep_num_tokens(const ep_handle* h);
  * multiple of 4 (16-byte aligned columns). */
 int64_t ep_scale_ld(const ep_handle* h);
 
+/* The router before ep_layout: each token's top_k experts and their weights
+ * from its logits.  Needs no handle.
+ *   logits        device fp32 (EP_ROUTE_BF16: bf16) [num_tokens, num_experts],
+ *                 rows logits_ld >= num_experts values apart.
+ *   num_experts   1..1024; top_k 1..32, at most num_experts.
+ *   flags         scores are the softmax over all experts of the token, with
+ *                 EP_ROUTE_SIGMOID 1 / (1 + exp(-logit)); EP_ROUTE_NORMALIZE
+ *                 divides a token's weights by their sum.
+ *   bias          device fp32 [num_experts] or NULL, with EP_ROUTE_SIGMOID only
+ *                 (else EP_ERR_UNSUPPORTED): added to the scores for the choice,
+ *                 not to the weights.
+ *   scale         factor of every weight.
+ *   topk_idx      device int32 [num_tokens, top_k], topk_weights device fp32
+ *                 [num_tokens, top_k]: what ep_layout takes.
+ * The experts come in descending order of their scores, equal ones with the
+ * lowest number first; biased scores are compared in double.  A logit (or a
+ * bias) of -inf or NaN closes the expert to the token; slots that no open
+ * expert is left for get index -1 and weight 0.  +inf counts as the largest
+ * finite logit.  One launch; capturable. */
+#define EP_ROUTE_BF16      (1u << 11)
+#define EP_ROUTE_SIGMOID   (1u << 12)
+#define EP_ROUTE_NORMALIZE (1u << 13)
+ep_status ep_route(const void* logits, int64_t logits_ld, int32_t num_tokens, int32_t num_experts, int32_t top_k,
+                   uint32_t flags, const float* bias, float scale, int32_t* topk_idx, float* topk_weights,
+                   hipStream_t stream);
+
+/* Backward of ep_route: the logits' gradient from that of the weights (as
+ * ep_combine_backward writes it).  logits, flags and scale as in the forward
+ * call; topk_idx is what it chose (the choice itself has no gradient; slots
+ * outside [0, num_experts) and closed experts count as masked).
+ *   grad_logits   device, the logits' type, [num_tokens, num_experts], rows
+ *                 grad_ld >= num_experts values apart; fully written, must not
+ *                 share memory with the inputs. */
+ep_status ep_route_backward(const void* logits, int64_t logits_ld, int32_t num_tokens, int32_t num_experts,
+                            int32_t top_k, uint32_t flags, float scale, const int32_t* topk_idx,
+                            const float* grad_weights, void* grad_logits, int64_t grad_ld, hipStream_t stream);
+
 /* Build the expert-major layout of one routing ([SEP], [ROUND]).
  *   topk_idx      device int32 [num_tokens, top_k]; -1 marks a masked slot.
  *   topk_weights  device fp32  [num_tokens, top_k]; copied into the handle.
@@ -399,6 +436,62 @@ ep_status ep_expert_ffn_backward(const ep_handle* h, uint32_t epoch, const void*
                                  int32_t activation, const void* act, const float* gate_up, uint32_t flags,
                                  void* grad_gate_up, void* grad_pool, void* grad_w_gate_up,
                                  void* grad_w_down, hipStream_t stream);
+
+/* One AdamW step over many tensors (decoupled weight decay), the experts'
+ * weights with the gradients of ep_expert_ffn_backward among them.  Per value,
+ * with g the gradient times grad_scale:
+ *     m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *     p = p (1 - lr weight_decay)
+ *         - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * in fp32, each result rounded once.  Needs no handle.
+ *   tensors   host array of `count` entries; read before the call returns.
+ *     param        device fp32 (EP_ADAMW_PARAM_BF16: bf16) [n], updated.
+ *     grad         device fp32 (EP_ADAMW_GRAD_BF16: bf16) [n].
+ *     exp_avg, exp_avg_sq   device fp32 [n]: m and v, updated.  With
+ *                  EP_ADAMW_STATE_8BIT e4m3fn bytes [n] of m and of sqrt(v), in
+ *                  the float32 scale flavour of the FP8 dispatch
+ *                  (EP_SCALE_F32) over each 128 values in order, the last
+ *                  block possibly shorter; a root above zero never gets code 0.
+ *                  An infinity makes its block of 128 NaN, as one scale holds it.
+ *     exp_avg_scale, exp_avg_sq_scale   device fp32 [ceil(n / 128)] with
+ *                  EP_ADAMW_STATE_8BIT, else NULL.
+ *     copy         device bf16 [n] or NULL: receives the updated fp32 parameter
+ *                  rounded (with fp32 parameters only, else EP_ERR_UNSUPPORTED).
+ *     n            >= 0, any.  Buffers are 16-byte aligned, scales 4-byte.
+ *   cfg       host.  step >= 1, or step_dev (device int64, read when the step
+ *             runs: a replayed graph takes the value it then holds; 8-byte
+ *             aligned) instead; grad_scale_dev (device fp32 or NULL) is a further
+ *             factor of the gradients, read when the step runs.  0 <= beta < 1,
+ *             eps >= 0.
+ * A buffer that is written must not share memory with any other, the same
+ * tensor twice included (EP_ERR_INVALID_ARGUMENT).  One launch for each 52
+ * tensors; capturable (the host's numbers are those of the capture). */
+#define EP_ADAMW_PARAM_BF16 (1u << 14)
+#define EP_ADAMW_GRAD_BF16  (1u << 15)
+#define EP_ADAMW_STATE_8BIT (1u << 16)
+typedef struct ep_adamw_tensor {
+    void* param;
+    const void* grad;
+    void* exp_avg;
+    void* exp_avg_sq;
+    float* exp_avg_scale;
+    float* exp_avg_sq_scale;
+    void* copy;
+    int64_t n;
+} ep_adamw_tensor;
+typedef struct ep_adamw_config {
+    double lr;
+    double beta1;
+    double beta2;
+    double eps;
+    double weight_decay;
+    int64_t step;
+    const int64_t* step_dev;
+    const float* grad_scale_dev;
+    float grad_scale;
+    uint32_t flags;
+} ep_adamw_config;
+ep_status ep_adamw(const ep_adamw_tensor* tensors, int32_t count, const ep_adamw_config* cfg, hipStream_t stream);
 
 /* End the lease of a borrowing dispatch ([BORROW]).  consumer_stream is the
  * stream the consumers of the view were enqueued on; the handle's next call
