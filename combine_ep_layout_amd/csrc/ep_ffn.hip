@@ -14,13 +14,14 @@
 // or a rounding).
 //
 // Operands go from memory straight into LDS (16 bytes a lane, no registers),
-// ST tiles of 64 summed indices deep.  Where the summed index is contiguous a
+// ST tiles of 32 or 64 summed indices deep.  Where the summed index is contiguous a
 // fragment is one ds_read_b128; where it is not, the tile keeps the memory's
 // order and two transposing reads (ds_read_b64_tr_b16) make the fragment, so
 // no operand is transposed in memory.  Both layouts are swizzled by permuting
 // which 16 bytes a lane fetches, since the load itself fills LDS linearly.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+#include <utility>
 
 #include "ep_ffn.h"
 
@@ -35,7 +36,6 @@ typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) char lds_char;
 
 constexpr int kWave = 64;
-constexpr int BK = 64;                      // summed indices of one LDS tile
 constexpr uint32_t kOutOfRange = 0x80000000u;   // offset past every buffer's range: such a lane loads zeros
 constexpr int kMaxExperts = 1024;
 constexpr int kXcds = 8;
@@ -46,6 +46,14 @@ enum Op { kUp, kDown, kActGrad, kRowGrad, kWeightGrad };
 
 constexpr bool a_strided(int op) { return op == kWeightGrad; }
 constexpr bool b_strided(int op) { return op == kActGrad || op == kRowGrad || op == kWeightGrad; }
+
+// f(0), ..., f(N - 1) with constant arguments.
+template <class F, int... I>
+__device__ __forceinline__ void each_of(F&& f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void each(F&& f) { each_of(f, std::make_integer_sequence<int, N>{}); }
 
 __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
@@ -81,16 +89,21 @@ __device__ __forceinline__ int strided_swizzle(int k) {
     constexpr int mask = (R / 16 < 8 ? R / 16 : 8) - 1;
     return ((k & 3) | ((k >> 1) & 4)) & mask;
 }
+// Swizzle of a contiguous tile's row r, BK values of it: the 16-byte chunks
+// that eight rows read together lie in different banks.
+template <int BK>
+__device__ __forceinline__ int row_swizzle(int r) {
+    return BK == 64 ? r & 7 : (r >> 1) & 3;
+}
 
-// Loads of one operand's LDS tile by one wave.
-//   STRIDED false: R rows of 64 summed values; true: 64 rows of R columns.
-template <int R, bool STRIDED, int WAVES>
+// Loads of one operand's LDS tile, BK summed indices deep, by one wave.
+//   STRIDED false: R rows of BK summed values; true: BK rows of R columns.
+template <int R, int BK, bool STRIDED, int WAVES>
 struct Loader {
-    static constexpr int kTotal = R / 8;                              // 1 KiB loads of a tile
+    static constexpr int kTotal = R * BK / 512;                       // 1 KiB loads of a tile
     static constexpr int kLoads = kTotal / WAVES > 0 ? kTotal / WAVES : 1;   // each wave's
     uint32_t voff[kLoads];
-    int k[kLoads];              // summed index of the lane's first value inside the tile
-    i32x4 rsrc;
+    int lane_k;                 // summed index of the lane's first value inside a load's part of the tile
     uint64_t base, step;
 
     __device__ __forceinline__ static int load_index(int wave, int i) {
@@ -104,38 +117,42 @@ struct Loader {
         for (int i = 0; i < kLoads; ++i) {
             const int g = load_index(wave, i);
             if constexpr (!STRIDED) {
-                const int r = lane >> 3, c = (lane & 7) ^ r;
-                voff[i] = row(g * 8 + r) + c * 16;
-                k[i] = c * 8;
+                constexpr int kChunks = BK / 8;
+                const int r = lane / kChunks, c = (lane % kChunks) ^ row_swizzle<BK>(r);
+                voff[i] = row(g * (kWave / kChunks) + r) + c * 16;
+                lane_k = c * 8;
             } else {
                 constexpr int kRows = 512 / R;
                 const int kk = g * kRows + lane / (R / 8), c = lane % (R / 8);
                 const int src = (((c >> 1) ^ strided_swizzle<R>(kk)) << 1) | (c & 1);
                 voff[i] = (uint32_t)kk * ld_bytes + row(src);
-                k[i] = kk;
+                lane_k = lane / (R / 8);
             }
         }
         base = (uint64_t)(uintptr_t)p;
         step = STRIDED ? (uint64_t)ld_bytes * BK : BK * 2;
     }
     // rem: summed indices left from this tile on (may be <= 0: zeros)
+    __device__ __forceinline__ void issue_one(int i, uint32_t lds, int wave, int rem, const i32x4& rsrc) const {
+        const int g = load_index(wave, i), first = STRIDED ? g * (512 / R) : 0;
+        load_to_lds(uni(lds + g * 1024), lane_k < rem - first ? voff[i] : kOutOfRange, rsrc);
+    }
     __device__ __forceinline__ void issue(uint32_t lds, int wave, int rem) {
-        rsrc = make_rsrc((const void*)(uintptr_t)base);
+        const i32x4 rsrc = make_rsrc((const void*)(uintptr_t)base);
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-            load_to_lds(uni(lds + load_index(wave, i) * 1024), k[i] < rem ? voff[i] : kOutOfRange, rsrc);
+        for (int i = 0; i < kLoads; ++i) issue_one(i, lds, wave, rem, rsrc);
         base += step;
     }
 };
 
 // A fragment for the matrix core: 16 rows (or columns) from `at`, summed
 // indices 32 s + 8 (lane / 16) + 0..7.
-template <int R, bool STRIDED>
+template <int R, int BK, bool STRIDED>
 __device__ __forceinline__ bf16x8 fragment(lds_char* tile, int at, int s, int lane) {
     if constexpr (!STRIDED) {
         const int r = at + (lane & 15);
-        const int c = (s * 4 + (lane >> 4)) ^ (lane & 7);       // at is a multiple of 16
-        return *(__attribute__((address_space(3))) bf16x8*)(tile + r * 128 + c * 16);
+        const int c = (s * 4 + (lane >> 4)) ^ row_swizzle<BK>(lane & 15);       // at is a multiple of 16
+        return *(__attribute__((address_space(3))) bf16x8*)(tile + r * (BK * 2) + c * 16);
     } else {
         const int k = s * 32 + (lane >> 4) * 8 + ((lane & 15) >> 2);
         // rows k and k + 4 have the same swizzle
@@ -181,27 +198,299 @@ __device__ __forceinline__ bf16x4 round4(const f32x4& v) {
     return r;
 }
 
-// BM x BN tiles, WM x WN of it to each wave, ST LDS tiles of each operand.
-template <int OP, int BM, int BN, int WM, int WN, int ST>
+// BM x BN tiles, WM x WN of it to each wave, ST LDS tiles of each operand, BK
+// summed indices deep.
+template <int OP_, int BM_, int BN_, int WM_, int WN_, int BK_, int ST_, bool PIPELINED = false>
 struct Shape {
+    static constexpr int OP = OP_, BM = BM_, BN = BN_, WM = WM_, WN = WN_, BK = BK_, ST = ST_;
     static constexpr int kWaves = (BM / WM) * (BN / WN);
     static constexpr int kThreads = kWaves * kWave;
     static constexpr int kStageBytes = (BM + BN) * BK * 2;
     static constexpr int kCols = OP == kUp ? BN / 2 : BN;       // output columns of a tile
+    // kUp: gate columns and then their up columns, in groups of this many
+    static constexpr int kPair = 32;
+    static constexpr bool kPipelined = PIPELINED;
+    using A = Loader<BM, BK, a_strided(OP), kWaves>;
+    using B = Loader<BN, BK, b_strided(OP), kWaves>;
+    static constexpr int kLoads = A::kLoads + B::kLoads;
     static constexpr size_t lds() { return (size_t)ST * kStageBytes + (kMaxExperts + 1 + 16) * sizeof(int); }
 };
 
-template <int OP, int BM, int BN, int WM, int WN, int ST>
-__global__ void __launch_bounds__((Shape<OP, BM, BN, WM, WN, ST>::kThreads))
-ffn_gemm_kernel(GemmArgs p) {
-    using S = Shape<OP, BM, BN, WM, WN, ST>;
-    constexpr bool AS = a_strided(OP), BS = b_strided(OP);
-    constexpr int MF = WM / 16, NF = WN / 16;
+// One tile of one expert.
+struct Tile {
+    int e, cnt, m0, n0;
+    int64_t region;             // the expert's first pool row
+};
+
+// A row's values of a fragment pair, columns c0.. of the first and c1.. of the
+// second (16 each), rounded to bf16.  Lane l holds row l % 16 and columns
+// 4 (l / 16) + 0..3; the lanes of odd rows of 16 trade their first half for the
+// even ones' second, so that each stores 16 bytes.
+__device__ __forceinline__ void store_pair(__bf16* out, int c0, int c1, int cols, int lane, const f32x4& v0, const f32x4& v1) {
+    union { bf16x4 h[2]; uint32_t w[4]; i32x4 q; } x;
+    x.h[0] = round4(v0);
+    x.h[1] = round4(v1);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const auto r = __builtin_amdgcn_permlane16_swap(x.w[i], x.w[2 + i], false, false);
+        x.w[i] = r[0];
+        x.w[2 + i] = r[1];
+    }
+    const int c = ((lane & 16) ? c1 : c0) + (lane >> 5) * 8;
+    if (c < cols) *(i32x4*)(out + c) = x.q;
+}
+__device__ __forceinline__ void store_one(__bf16* out, int c, int cols, const f32x4& v) {
+    if (c < cols) *(bf16x4*)(out + c) = round4(v);
+}
+
+// Writes a wave's part of the finished tile: rows from r_at, tile columns from c_at.
+template <class S, int MF, int NF>
+__device__ __forceinline__ void finish(const GemmArgs& p, const Tile& t, int r_at, int c_at, int lane,
+                                       const f32x4 (&acc)[MF][NF]) {
+    constexpr int OP = S::OP;
+    const int r0 = t.m0 + r_at + (lane & 15), c_in = (lane >> 4) * 4;
+    const int rows = OP == kWeightGrad ? p.M : t.cnt;
+#pragma unroll
+    for (int i = 0; i < MF; ++i) {
+        const int r = r0 + i * 16;
+        // lanes of a row past the end take part in the exchange, but not in the stores
+        const int cols = r < rows ? p.N : 0;
+        if constexpr (OP == kUp) {
+            // fragments j, j + 1: 16 gate columns and their up columns
+            __bf16* out = (__bf16*)p.c + (t.region + r) * (int64_t)p.N;
+            f32x4 v[NF / 2];
+#pragma unroll
+            for (int j = 0; j < NF / 2; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[j][q] = act_value(acc[i][2 * j][q], p.act) * acc[i][2 * j + 1][q];
+            const int c = t.n0 + (c_at >> 1);
+            if constexpr (NF == 2) {
+                store_one(out, c + c_in, cols, v[0]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < NF / 2; j += 2) store_pair(out, c + j * 16, c + j * 16 + 16, cols, lane, v[j], v[j + 1]);
+            }
+            if (p.save) {
+                float* save = (float*)p.save + (t.region + r) * (int64_t)(2 * p.N);
+#pragma unroll
+                for (int j = 0; j < NF / 2; ++j)
+                    if (c + j * 16 + c_in < cols) {
+                        *(f32x4*)(save + c + j * 16 + c_in) = acc[i][2 * j];
+                        *(f32x4*)(save + p.N + c + j * 16 + c_in) = acc[i][2 * j + 1];
+                    }
+            }
+        } else if constexpr (OP == kActGrad) {
+            const float* saved = (const float*)p.save + (t.region + r) * (int64_t)(2 * p.N);
+            __bf16* out = (__bf16*)p.c + (t.region + r) * (int64_t)(2 * p.N);
+            f32x4 dg[NF], du[NF];
+#pragma unroll
+            for (int j = 0; j < NF; ++j) {
+                const int c = t.n0 + c_at + j * 16 + c_in;
+                f32x4 g{0.f, 0.f, 0.f, 0.f}, u = g;
+                if (c < cols) {
+                    g = *(const f32x4*)(saved + c);
+                    u = *(const f32x4*)(saved + p.N + c);
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float value, slope;
+                    act_both(g[q], p.act, value, slope);
+                    dg[j][q] = acc[i][j][q] * u[q] * slope;
+                    du[j][q] = acc[i][j][q] * value;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < NF; j += 2) {
+                const int c = t.n0 + c_at + j * 16;
+                store_pair(out, c, c + 16, cols, lane, dg[j], dg[j + 1]);
+                store_pair(out + p.N, c, c + 16, cols, lane, du[j], du[j + 1]);
+            }
+        } else {
+            const int64_t at = OP == kWeightGrad ? ((int64_t)t.e * p.M + r) * p.N : (t.region + r) * (int64_t)p.N;
+            if (OP == kWeightGrad && p.out_f32) {
+#pragma unroll
+                for (int j = 0; j < NF; ++j) {
+                    const int c = t.n0 + c_at + j * 16 + c_in;
+                    if (c >= cols) continue;
+                    f32x4* o = (f32x4*)((float*)p.c + at + c);
+                    f32x4 v = acc[i][j];
+                    if (p.accumulate) {
+                        const f32x4 old = *o;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) v[q] += old[q];
+                    }
+                    *o = v;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < NF; j += 2)
+                    store_pair((__bf16*)p.c + at, t.n0 + c_at + j * 16, t.n0 + c_at + j * 16 + 16, cols, lane, acc[i][j], acc[i][j + 1]);
+            }
+        }
+    }
+}
+
+// c += b a^T in the accumulation registers.  Written out, since the compiler
+// moves 256 of those about at every turn of the loop.  s_nop 1: the states a
+// vector instruction's result needs before the matrix core reads it.
+__device__ __forceinline__ void mfma(f32x4& c, const bf16x8& b, const bf16x8& a) {
+    asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(b), "v"(a));
+}
+// The states that the matrix core's results need before another instruction
+// reads them (18 at most), for a row of fragments.
+__device__ __forceinline__ void settle(f32x4 (&c)[8]) {
+    asm volatile("s_nop 15\n\ts_nop 3"
+                 : "+a"(c[0]), "+a"(c[1]), "+a"(c[2]), "+a"(c[3]), "+a"(c[4]), "+a"(c[5]), "+a"(c[6]), "+a"(c[7]));
+}
+__device__ __forceinline__ void settle(f32x4 (&c)[2]) {
+    asm volatile("s_nop 15\n\ts_nop 3" : "+a"(c[0]), "+a"(c[1]));
+}
+__device__ __forceinline__ void settle(f32x4 (&c)[4]) {
+    asm volatile("s_nop 15\n\ts_nop 3" : "+a"(c[0]), "+a"(c[1]), "+a"(c[2]), "+a"(c[3]));
+}
+
+template <int MF, int NF>
+struct Fragments {
+    bf16x8 a[MF], b[NF];
+};
+
+// A wave's MF x NF fragments of a tile, from tile row r_at and column c_at,
+// summed over K, in a software pipeline over halves of 32 summed indices.
+// While the matrix core works on one half from registers, the wave reads the
+// next half's fragments from LDS; after a tile's second half has been read,
+// its LDS takes the loads of the tile after next.  One barrier a tile.
+template <class S, int MF, int NF>
+__device__ __forceinline__ void pipelined_tile(const GemmArgs& p, const Tile& t, typename S::A& la, typename S::B& lb,
+                                               int K, int r_at, int c_at, int wave, int lane, lds_char* lds) {
+    static_assert(S::BK == 64 && S::ST == 2, "two tiles of two halves");
+    constexpr bool AS = a_strided(S::OP), BS = b_strided(S::OP);
+    constexpr int LA = S::A::kLoads, L = S::kLoads;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+    const int nk = (K + S::BK - 1) / S::BK;
+    f32x4 acc[MF][NF];
+#pragma unroll
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int j = 0; j < NF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const uint32_t at = lds0 + s * S::kStageBytes;
+        la.issue(at, wave, K - s * S::BK);
+        lb.issue(at + S::BM * S::BK * 2, wave, K - s * S::BK);
+    }
+    Fragments<MF, NF> f0, f1;
+    wait_loads<L>();
+    __builtin_amdgcn_s_barrier();
+    auto read_a = [&](int i, int slot, int s) {
+        return fragment<S::BM, S::BK, AS>(lds + slot * S::kStageBytes, r_at + i * 16, s, lane);
+    };
+    auto read_b = [&](int j, int slot, int s) {
+        return fragment<S::BN, S::BK, BS>(lds + slot * S::kStageBytes + S::BM * S::BK * 2, c_at + j * 16, s, lane);
+    };
+#pragma unroll
+    for (int j = 0; j < NF; ++j) f0.b[j] = read_b(j, 0, 0);
+#pragma unroll
+    for (int i = 0; i < MF; ++i) f0.a[i] = read_a(i, 0, 0);
+    // The products of `now`, with the reads of `next` (half s of an LDS tile)
+    // and, LOAD, this wave's loads of a tile spread between them: the matrix
+    // core takes 16 cycles for a product and an instruction of another kind 4,
+    // so one or two behind each product are free.
+    auto half = [&](auto load, const Fragments<MF, NF>& now, Fragments<MF, NF>& next, int slot, int s, uint32_t fill, int rem) {
+        constexpr bool LOAD = decltype(load)::value;
+        const i32x4 ra = make_rsrc((const void*)(uintptr_t)la.base), rb = make_rsrc((const void*)(uintptr_t)lb.base);
+        each<MF * NF>([&](auto product) {
+            constexpr int n = product, P = MF * NF, F = MF + NF;
+            mfma(acc[n / NF][n % NF], now.b[n % NF], now.a[n / NF]);
+            // both end well before the half, so that the last have come when they are needed
+            constexpr int R = P * 3 / 4, r0 = n * F / R < F ? n * F / R : F, r1 = (n + 1) * F / R < F ? (n + 1) * F / R : F;
+            each<r1 - r0>([&](auto i) {
+                constexpr int r = r0 + i;
+                if constexpr (r < NF) next.b[r] = read_b(r, slot, s);
+                else next.a[r - NF] = read_a(r - NF, slot, s);
+            });
+            if constexpr (LOAD) {
+                constexpr int Q = P / 2, l0 = n * L / Q < L ? n * L / Q : L, l1 = (n + 1) * L / Q < L ? (n + 1) * L / Q : L;
+                each<l1 - l0>([&](auto i) {
+                    constexpr int l = l0 + i;
+                    if constexpr (l < LA) la.issue_one(l, fill, wave, rem, ra);
+                    else lb.issue_one(l - LA, fill + S::BM * S::BK * 2, wave, rem, rb);
+                });
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        if constexpr (LOAD) {
+            la.base += la.step;
+            lb.base += lb.step;
+        }
+    };
+#pragma unroll 1
+    for (int kt = 0; kt < nk; ++kt) {
+        const int slot = kt & 1;
+        half(std::false_type{}, f0, f1, slot, 1, 0, 0);
+        // this tile's second half has come to registers, and the next tile to
+        // LDS; after the barrier that holds for every wave
+        wait_loads<0>();
+        __builtin_amdgcn_s_barrier();
+        half(std::true_type{}, f1, f0, slot ^ 1, 0, lds0 + slot * S::kStageBytes, K - (kt + 2) * S::BK);
+    }
+#pragma unroll
+    for (int i = 0; i < MF; ++i) settle(acc[i]);
+    finish<S, MF, NF>(p, t, r_at, c_at, lane, acc);
+}
+
+// The same without the register pipeline, for tiles few rows high: those are
+// bound by the weights' bytes, and several workgroups of a compute unit hide
+// each other's waits.
+template <class S>
+__device__ __forceinline__ void plain_tile(const GemmArgs& p, const Tile& t, typename S::A& la, typename S::B& lb, int K,
+                                           int r_at, int c_at, int wave, int lane, lds_char* lds) {
+    constexpr bool AS = a_strided(S::OP), BS = b_strided(S::OP);
+    constexpr int MF = S::WM / 16, NF = S::WN / 16, ST = S::ST;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+    const int nk = (K + S::BK - 1) / S::BK;
+    f32x4 acc[MF][NF];
+#pragma unroll
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int j = 0; j < NF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto issue = [&](int kt) {
+        const uint32_t at = lds0 + (uint32_t)(kt % ST) * S::kStageBytes;
+        la.issue(at, wave, K - kt * S::BK);
+        lb.issue(at + S::BM * S::BK * 2, wave, K - kt * S::BK);
+    };
+#pragma unroll
+    for (int s = 0; s < ST - 1; ++s) issue(s);
+#pragma unroll 1
+    for (int kt = 0; kt < nk; ++kt) {
+        wait_loads<(ST - 2) * S::kLoads>();         // this wave's loads of tile kt
+        __builtin_amdgcn_s_barrier();               // every wave's; tile kt - 1 is read
+        issue(kt + ST - 1);
+        lds_char* at = lds + (kt % ST) * S::kStageBytes;
+#pragma unroll
+        for (int s = 0; s < S::BK / 32; ++s) {
+            bf16x8 fa[MF], fb[NF];
+#pragma unroll
+            for (int j = 0; j < NF; ++j) fb[j] = fragment<S::BN, S::BK, BS>(at + S::BM * S::BK * 2, c_at + j * 16, s, lane);
+#pragma unroll
+            for (int i = 0; i < MF; ++i) fa[i] = fragment<S::BM, S::BK, AS>(at, r_at + i * 16, s, lane);
+#pragma unroll
+            for (int i = 0; i < MF; ++i)
+#pragma unroll
+                for (int j = 0; j < NF; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+        }
+    }
+    finish<S, MF, NF>(p, t, r_at, c_at, lane, acc);
+}
+
+template <class S>
+__global__ void __launch_bounds__(S::kThreads) ffn_gemm_kernel(GemmArgs p) {
+    constexpr int OP = S::OP, BM = S::BM, BN = S::BN, WM = S::WM, WN = S::WN;
+    constexpr bool BS = b_strided(OP);
     extern __shared__ __attribute__((aligned(1024))) char smem[];
     lds_char* lds = (lds_char*)smem;
-    int* s_pref = (int*)(smem + ST * S::kStageBytes);
+    int* s_pref = (int*)(smem + S::ST * S::kStageBytes);
     const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
-    const int wm = wave / (BN / WN), wn = wave % (BN / WN);
     const int tiles_n = (p.N + S::kCols - 1) / S::kCols;
 
     int total;
@@ -244,26 +533,27 @@ ffn_gemm_kernel(GemmArgs p) {
     const int G = gridDim.x, per_xcd = G / kXcds;
     const int first = (G % kXcds == 0) ? (blockIdx.x % kXcds) * per_xcd + blockIdx.x / kXcds : blockIdx.x;
 
-    for (int t = first; t < total; t += G) {
-        int e, mt, nt;
+    for (int n = first; n < total; n += G) {
+        Tile t;
+        int mt, nt;
         {
             int local, tiles_m;
             if constexpr (OP == kWeightGrad) {
                 tiles_m = (p.M + BM - 1) / BM;
-                e = t / (tiles_m * tiles_n);
-                local = t - e * tiles_m * tiles_n;
+                t.e = n / (tiles_m * tiles_n);
+                local = n - t.e * tiles_m * tiles_n;
             } else {
-                const int key = t / tiles_n;
+                const int key = n / tiles_n;
                 int lo = 0, hi = p.E;               // s_pref[lo] <= key < s_pref[hi]
                 while (hi - lo > 1) {
                     const int mid = (lo + hi) >> 1;
                     if (s_pref[mid] <= key) lo = mid;
                     else hi = mid;
                 }
-                e = uni(lo);
-                const int before = uni(s_pref[e]);
-                tiles_m = uni(s_pref[e + 1]) - before;
-                local = t - before * tiles_n;
+                t.e = uni(lo);
+                const int before = uni(s_pref[t.e]);
+                tiles_m = uni(s_pref[t.e + 1]) - before;
+                local = n - before * tiles_n;
             }
             const int grp = local / (kGroupM * tiles_n);
             const int in = local - grp * kGroupM * tiles_n;
@@ -271,173 +561,81 @@ ffn_gemm_kernel(GemmArgs p) {
             nt = in / rows;
             mt = grp * kGroupM + in - nt * rows;
         }
-        const int cnt = uni(p.counts[e]);
-        const int64_t region = (int64_t)uni(p.offsets[e]) * p.block_m;
-        const int K = OP == kWeightGrad ? cnt : p.K;
-        const int m0 = mt * BM, n0 = nt * S::kCols;
-        const int nk = (K + BK - 1) / BK;
+        t.cnt = uni(p.counts[t.e]);
+        t.region = (int64_t)uni(p.offsets[t.e]) * p.block_m;
+        t.m0 = mt * BM;
+        t.n0 = nt * S::kCols;
+        const int K = OP == kWeightGrad ? t.cnt : p.K;
 
-        Loader<BM, AS, S::kWaves> la;
-        Loader<BN, BS, S::kWaves> lb;
+        typename S::A la;
+        typename S::B lb;
         const uint32_t a_ldb = (uint32_t)p.a_ld * 2, b_ldb = (uint32_t)p.b_ld * 2;
         if constexpr (OP == kWeightGrad) {
             // columns past the matrix repeat its last chunk; they are not stored
             const int a_last = (p.M >> 3) - 1, b_last = (p.N >> 3) - 1;
-            la.init((const char*)p.a + region * a_ldb, a_ldb, wave, lane, [&](int c) {
-                const int g = (m0 >> 3) + c;
+            la.init((const char*)p.a + t.region * a_ldb, a_ldb, wave, lane, [&](int c) {
+                const int g = (t.m0 >> 3) + c;
                 return (uint32_t)(g < a_last ? g : a_last) * 16u;
             });
-            lb.init((const char*)p.b + region * b_ldb, b_ldb, wave, lane, [&](int c) {
-                const int g = (n0 >> 3) + c;
+            lb.init((const char*)p.b + t.region * b_ldb, b_ldb, wave, lane, [&](int c) {
+                const int g = (t.n0 >> 3) + c;
                 return (uint32_t)(g < b_last ? g : b_last) * 16u;
             });
         } else {
             // rows past the region repeat its last row; they are not stored
-            const int last = cnt - 1 - m0;
-            la.init((const char*)p.a + (region + m0) * a_ldb, a_ldb, wave, lane,
+            const int last = t.cnt - 1 - t.m0;
+            la.init((const char*)p.a + (t.region + t.m0) * a_ldb, a_ldb, wave, lane,
                     [&](int r) { return (uint32_t)(r < last ? r : last) * a_ldb; });
-            const char* b = (const char*)p.b + (int64_t)e * p.b_expert * 2;
+            const char* b = (const char*)p.b + (int64_t)t.e * p.b_expert * 2;
             if constexpr (OP == kUp) {
-                // gate columns, then the up columns that belong to them, per wave
                 lb.init(b, b_ldb, wave, lane, [&](int r) {
-                    const int j = r % WN, up = j >= WN / 2;
-                    int c = n0 + r / WN * (WN / 2) + j % (WN / 2);
+                    constexpr int P = S::kPair;
+                    const int j = r % P, up = j >= P / 2;
+                    int c = t.n0 + r / P * (P / 2) + j % (P / 2);
                     c = c < p.N ? c : p.N - 1;
                     return (uint32_t)(up ? p.N + c : c) * b_ldb;
                 });
             } else if constexpr (!BS) {
                 lb.init(b, b_ldb, wave, lane, [&](int r) {
-                    const int c = n0 + r;
+                    const int c = t.n0 + r;
                     return (uint32_t)(c < p.N ? c : p.N - 1) * b_ldb;
                 });
             } else {
                 const int b_last = (p.N >> 3) - 1;
                 lb.init(b, b_ldb, wave, lane, [&](int c) {
-                    const int g = (n0 >> 3) + c;
+                    const int g = (t.n0 >> 3) + c;
                     return (uint32_t)(g < b_last ? g : b_last) * 16u;
                 });
             }
         }
 
-        const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
-        auto issue = [&](int kt) {
-            const uint32_t at = lds0 + (uint32_t)(kt % ST) * S::kStageBytes;
-            la.issue(at, wave, K - kt * BK);
-            lb.issue(at + BM * BK * 2, wave, K - kt * BK);
-        };
-        constexpr int kLoads = Loader<BM, AS, S::kWaves>::kLoads + Loader<BN, BS, S::kWaves>::kLoads;
-
-        f32x4 acc[MF][NF];
-#pragma unroll
-        for (int i = 0; i < MF; ++i)
-#pragma unroll
-            for (int j = 0; j < NF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
         // the last tile's reads are done before its LDS is filled again
         wait_loads<0>();
         __builtin_amdgcn_s_barrier();
-#pragma unroll
-        for (int s = 0; s < ST - 1; ++s) issue(s);
-#pragma unroll 1
-        for (int kt = 0; kt < nk; ++kt) {
-            wait_loads<(ST - 2) * kLoads>();            // this wave's loads of tile kt
-            __builtin_amdgcn_s_barrier();               // every wave's; tile kt - 1 is read
-            issue(kt + ST - 1);
-            lds_char* at = lds + (kt % ST) * S::kStageBytes;
-#pragma unroll
-            for (int s = 0; s < BK / 32; ++s) {
-                bf16x8 fa[MF], fb[NF];
-#pragma unroll
-                for (int j = 0; j < NF; ++j) fb[j] = fragment<BN, BS>(at + BM * BK * 2, wn * WN + j * 16, s, lane);
-#pragma unroll
-                for (int i = 0; i < MF; ++i) fa[i] = fragment<BM, AS>(at, wm * WM + i * 16, s, lane);
-#pragma unroll
-                for (int i = 0; i < MF; ++i)
-#pragma unroll
-                    for (int j = 0; j < NF; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
-            }
-        }
-
-        // Lane l holds row l % 16 and columns 4 (l / 16) + 0..3 of a fragment.
-        const int r0 = m0 + wm * WM + (lane & 15), c_in = (lane >> 4) * 4;
-        const int rows = OP == kWeightGrad ? p.M : cnt;
-#pragma unroll
-        for (int i = 0; i < MF; ++i) {
-            const int r = r0 + i * 16;
-            if (r >= rows) continue;
-            if constexpr (OP == kUp) {
-                __bf16* out = (__bf16*)p.c + (region + r) * (int64_t)p.N;
-                float* save = p.save ? (float*)p.save + (region + r) * (int64_t)(2 * p.N) : nullptr;
-#pragma unroll
-                for (int j = 0; j < NF / 2; ++j) {
-                    const int c = n0 + wn * (WN / 2) + j * 16 + c_in;
-                    if (c >= p.N) continue;
-                    const f32x4 g = acc[i][j], u = acc[i][j + NF / 2];
-                    f32x4 v;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) v[q] = act_value(g[q], p.act) * u[q];
-                    *(bf16x4*)(out + c) = round4(v);
-                    if (save) {
-                        *(f32x4*)(save + c) = g;
-                        *(f32x4*)(save + p.N + c) = u;
-                    }
-                }
-            } else if constexpr (OP == kActGrad) {
-                const float* saved = (const float*)p.save + (region + r) * (int64_t)(2 * p.N);
-                __bf16* out = (__bf16*)p.c + (region + r) * (int64_t)(2 * p.N);
-#pragma unroll
-                for (int j = 0; j < NF; ++j) {
-                    const int c = n0 + wn * WN + j * 16 + c_in;
-                    if (c >= p.N) continue;
-                    const f32x4 g = *(const f32x4*)(saved + c), u = *(const f32x4*)(saved + p.N + c);
-                    f32x4 dg, du;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float value, slope;
-                        act_both(g[q], p.act, value, slope);
-                        dg[q] = acc[i][j][q] * u[q] * slope;
-                        du[q] = acc[i][j][q] * value;
-                    }
-                    *(bf16x4*)(out + c) = round4(dg);
-                    *(bf16x4*)(out + p.N + c) = round4(du);
-                }
-            } else {
-                const int64_t at = OP == kWeightGrad ? ((int64_t)e * p.M + r) * p.N : (region + r) * (int64_t)p.N;
-#pragma unroll
-                for (int j = 0; j < NF; ++j) {
-                    const int c = n0 + wn * WN + j * 16 + c_in;
-                    if (c >= p.N) continue;
-                    if (OP == kWeightGrad && p.out_f32) {
-                        f32x4* o = (f32x4*)((float*)p.c + at + c);
-                        f32x4 v = acc[i][j];
-                        if (p.accumulate) {
-                            const f32x4 old = *o;
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) v[q] += old[q];
-                        }
-                        *o = v;
-                    } else {
-                        *(bf16x4*)((__bf16*)p.c + at + c) = round4(acc[i][j]);
-                    }
-                }
-            }
+        constexpr int kAcross = BN / WN;
+        if constexpr (S::kPipelined) {
+            // a tile whose lower half has no rows is shared out by columns alone
+            if (OP != kWeightGrad && BM == 2 * WM && t.cnt - t.m0 <= WM)
+                pipelined_tile<S, WM / 16, WN / 32>(p, t, la, lb, K, 0, wave * (WN / 2), wave, lane, lds);
+            else
+                pipelined_tile<S, WM / 16, WN / 16>(p, t, la, lb, K, wave / kAcross * WM, wave % kAcross * WN, wave, lane, lds);
+        } else {
+            plain_tile<S>(p, t, la, lb, K, wave / kAcross * WM, wave % kAcross * WN, wave, lane, lds);
         }
     }
     wait_loads<0>();        // no load into LDS outlives the workgroup
 }
 
-template <int OP, int BM, int BN, int WM, int WN, int ST>
+template <class S>
 hipError_t launch(const GemmArgs& p, int64_t row_tiles, hipStream_t stream) {
-    using S = Shape<OP, BM, BN, WM, WN, ST>;
-    auto kernel = ffn_gemm_kernel<OP, BM, BN, WM, WN, ST>;
     const int64_t tiles = row_tiles * ((p.N + S::kCols - 1) / S::kCols);
     if (tiles == 0) return hipSuccess;
     static_assert(S::lds() <= 160 * 1024, "LDS of a compute unit");
+    auto kernel = ffn_gemm_kernel<S>;
     hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)S::lds());
     if (e != hipSuccess) return e;
-    const int per_cu = (int)(160 * 1024 / S::lds());
-    const int64_t most = (int64_t)p.num_cu * (per_cu < 1 ? 1 : per_cu);
+    constexpr int kPerCu = 160 * 1024 / S::lds() < 1 ? 1 : (int)(160 * 1024 / S::lds());
+    const int64_t most = (int64_t)p.num_cu * kPerCu;
     const int grid = (int)(tiles < most ? tiles : most);
     kernel<<<grid, S::kThreads, S::lds(), stream>>>(p);
     return hipGetLastError();
@@ -452,10 +650,15 @@ int64_t row_tile_bound(const GemmArgs& p, int bm) {
 template <int OP>
 hipError_t launch_rows(const GemmArgs& p, hipStream_t stream) {
     const int64_t mean = (p.slots + p.E - 1) / p.E;
-    if (mean > 128) return launch<OP, 256, 256, 128, 64, 2>(p, row_tile_bound(p, 256), stream);
-    if (mean > 48) return launch<OP, 128, 128, 64, 64, 2>(p, row_tile_bound(p, 128), stream);
-    if (mean > 16) return launch<OP, 64, 128, 64, 32, 3>(p, row_tile_bound(p, 64), stream);
-    return launch<OP, 16, 128, 16, 32, 4>(p, row_tile_bound(p, 16), stream);
+    if (mean > 128) return launch<Shape<OP, 256, 256, 128, 64, 64, 2, true>>(p, row_tile_bound(p, 256), stream);
+    if (mean > 48) return launch<Shape<OP, 128, 128, 64, 64, 64, 2>>(p, row_tile_bound(p, 128), stream);
+    if (mean > 16) return launch<Shape<OP, 64, 128, 64, 32, 64, 3>>(p, row_tile_bound(p, 64), stream);
+    return launch<Shape<OP, 16, 128, 16, 32, 64, 4>>(p, row_tile_bound(p, 16), stream);
+}
+
+hipError_t launch_weight_grad(const GemmArgs& p, hipStream_t stream) {
+    using S = Shape<kWeightGrad, 256, 256, 128, 64, 64, 2, true>;
+    return launch<S>(p, (int64_t)p.E * ((p.M + S::BM - 1) / S::BM), stream);
 }
 
 GemmArgs rows_of(const FfnArgs& f) {
@@ -534,7 +737,7 @@ hipError_t launch_ffn_backward(const FfnArgs& f, hipStream_t stream) {
         p.c = f.grad_w_gate_up;
         p.M = 2 * f.I;
         p.N = f.H;
-        e = launch<kWeightGrad, 256, 256, 128, 64, 2>(p, (int64_t)f.E * ((p.M + 255) / 256), stream);
+        e = launch_weight_grad(p, stream);
         if (e != hipSuccess) return e;
     }
     if (f.grad_w_down) {
@@ -545,7 +748,7 @@ hipError_t launch_ffn_backward(const FfnArgs& f, hipStream_t stream) {
         p.c = f.grad_w_down;
         p.M = f.H;
         p.N = f.I;
-        e = launch<kWeightGrad, 256, 256, 128, 64, 2>(p, (int64_t)f.E * ((p.M + 255) / 256), stream);
+        e = launch_weight_grad(p, stream);
     }
     return e;
 }
