@@ -38,6 +38,7 @@ typedef __attribute__((address_space(3))) char lds_char;
 constexpr int kWave = 64;
 constexpr uint32_t kOutOfRange = 0x80000000u;   // offset past every buffer's range: such a lane loads zeros
 constexpr int kMaxExperts = 1024;
+constexpr size_t kLdsBytes = 160 * 1024;        // of a compute unit
 constexpr int kXcds = 8;
 constexpr int kGroupM = 8;                  // row tiles that share their column tiles' loads
 
@@ -213,7 +214,9 @@ struct Shape {
     using A = Loader<BM, BK, a_strided(OP), kWaves>;
     using B = Loader<BN, BK, b_strided(OP), kWaves>;
     static constexpr int kLoads = A::kLoads + B::kLoads;
-    static constexpr size_t lds() { return (size_t)ST * kStageBytes + (kMaxExperts + 1 + 16) * sizeof(int); }
+    static constexpr size_t kTileLds = (size_t)ST * kStageBytes;
+    // the scan of the row tiles follows the operands' tiles
+    static size_t lds(int E) { return kTileLds + (OP == kWeightGrad ? 0 : (size_t)(E + 1) * sizeof(int)); }
 };
 
 // One tile of one expert.
@@ -483,11 +486,11 @@ __device__ __forceinline__ void plain_tile(const GemmArgs& p, const Tile& t, typ
     finish<S, MF, NF>(p, t, r_at, c_at, lane, acc);
 }
 
+// All tiles of a product that fall to workgroup `block` of G.
 template <class S>
-__global__ void __launch_bounds__(S::kThreads) ffn_gemm_kernel(GemmArgs p) {
+__device__ __forceinline__ void run_product(const GemmArgs& p, int block, int G, char* smem) {
     constexpr int OP = S::OP, BM = S::BM, BN = S::BN, WM = S::WM, WN = S::WN;
     constexpr bool BS = b_strided(OP);
-    extern __shared__ __attribute__((aligned(1024))) char smem[];
     lds_char* lds = (lds_char*)smem;
     int* s_pref = (int*)(smem + S::ST * S::kStageBytes);
     const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
@@ -530,8 +533,8 @@ __global__ void __launch_bounds__(S::kThreads) ffn_gemm_kernel(GemmArgs p) {
 
     // Workgroup b runs on XCD b mod 8: consecutive tiles, which share rows and
     // columns, go to one XCD and its L2.
-    const int G = gridDim.x, per_xcd = G / kXcds;
-    const int first = (G % kXcds == 0) ? (blockIdx.x % kXcds) * per_xcd + blockIdx.x / kXcds : blockIdx.x;
+    const int per_xcd = G / kXcds;
+    const int first = (G % kXcds == 0) ? (block % kXcds) * per_xcd + block / kXcds : block;
 
     for (int n = first; n < total; n += G) {
         Tile t;
@@ -627,18 +630,31 @@ __global__ void __launch_bounds__(S::kThreads) ffn_gemm_kernel(GemmArgs p) {
 }
 
 template <class S>
-hipError_t launch(const GemmArgs& p, int64_t row_tiles, hipStream_t stream) {
-    const int64_t tiles = row_tiles * ((p.N + S::kCols - 1) / S::kCols);
-    if (tiles == 0) return hipSuccess;
-    static_assert(S::lds() <= 160 * 1024, "LDS of a compute unit");
-    auto kernel = ffn_gemm_kernel<S>;
-    hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)S::lds());
-    if (e != hipSuccess) return e;
-    constexpr int kPerCu = 160 * 1024 / S::lds() < 1 ? 1 : (int)(160 * 1024 / S::lds());
-    const int64_t most = (int64_t)p.num_cu * kPerCu;
-    const int grid = (int)(tiles < most ? tiles : most);
-    kernel<<<grid, S::kThreads, S::lds(), stream>>>(p);
-    return hipGetLastError();
+__global__ void __launch_bounds__(S::kThreads) ffn_gemm_kernel(GemmArgs p) {
+    extern __shared__ __attribute__((aligned(1024))) char smem[];
+    run_product<S>(p, blockIdx.x, gridDim.x, smem);
+}
+
+// The three products that follow the activation's gradient, for problems of
+// less than a round of tiles each: nothing is gained by their order then, and
+// two launches are saved.
+struct AfterArgs {
+    GemmArgs rows, gate_up, down;
+    int32_t grid_rows, grid_gate_up;        // workgroups of the first two
+};
+template <class R, class W>
+__global__ void __launch_bounds__(R::kThreads) ffn_after_kernel(AfterArgs a) {
+    static_assert(R::kThreads == W::kThreads, "one launch");
+    extern __shared__ __attribute__((aligned(1024))) char smem[];
+    const int b = blockIdx.x, n1 = a.grid_rows, n2 = n1 + a.grid_gate_up;
+    if (b < n1) run_product<R>(a.rows, b, n1, smem);
+    else if (b < n2) run_product<W>(a.gate_up, b - n1, n2 - n1, smem);
+    else run_product<W>(a.down, b - n2, (int)gridDim.x - n2, smem);
+}
+
+template <class K>
+hipError_t allow_lds(K* kernel, size_t lds) {
+    return hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
 }
 
 // Row tiles of height bm that the rows of the layout can need at most.
@@ -647,18 +663,69 @@ int64_t row_tile_bound(const GemmArgs& p, int bm) {
     return used + p.slots / bm;
 }
 
+template <class S>
+int64_t tile_count(const GemmArgs& p) {
+    const int64_t tiles_m = S::OP == kWeightGrad ? (int64_t)p.E * ((p.M + S::BM - 1) / S::BM) : row_tile_bound(p, S::BM);
+    return tiles_m * ((p.N + S::kCols - 1) / S::kCols);
+}
+
+template <class S>
+int grid_of(const GemmArgs& p) {
+    const int64_t tiles = tile_count<S>(p), most = (int64_t)p.num_cu * (int64_t)(kLdsBytes / S::lds(p.E));
+    return (int)(tiles < most ? tiles : most);
+}
+
+template <class S>
+hipError_t launch(const GemmArgs& p, hipStream_t stream) {
+    const int grid = grid_of<S>(p);
+    if (grid == 0) return hipSuccess;
+    static_assert(S::kTileLds + (kMaxExperts + 1) * sizeof(int) <= kLdsBytes, "LDS of a compute unit");
+    hipError_t e = allow_lds(ffn_gemm_kernel<S>, S::lds(p.E));
+    if (e != hipSuccess) return e;
+    ffn_gemm_kernel<S><<<grid, S::kThreads, S::lds(p.E), stream>>>(p);
+    return hipGetLastError();
+}
+
+// The tiles' shapes.  The widest, 256 x 256 with 8 waves and the register
+// pipeline, moves the fewest bytes through L2, which bounds these products;
+// it needs two rounds of tiles, or the last one leaves too many compute units
+// idle.
+template <int OP> using Wide = Shape<OP, 256, 256, 128, 64, 64, 2, true>;
+template <int OP> using Middle = Shape<OP, 128, 128, 64, 64, 64, 2>;
+template <int OP> using Low = Shape<OP, 64, 128, 64, 32, 64, 3>;
+template <int OP> using Small = Shape<OP, 64, 64, 32, 32, 64, 4>;
+template <int OP> using Few = Shape<OP, 16, 128, 16, 32, 64, 4>;
+
+template <int OP>
+bool is_small(const GemmArgs& p) {
+    return p.slots <= (int64_t)48 * p.E && p.slots > (int64_t)16 * p.E && tile_count<Low<OP>>(p) < p.num_cu;
+}
+
 template <int OP>
 hipError_t launch_rows(const GemmArgs& p, hipStream_t stream) {
     const int64_t mean = (p.slots + p.E - 1) / p.E;
-    if (mean > 128) return launch<Shape<OP, 256, 256, 128, 64, 64, 2, true>>(p, row_tile_bound(p, 256), stream);
-    if (mean > 48) return launch<Shape<OP, 128, 128, 64, 64, 64, 2>>(p, row_tile_bound(p, 128), stream);
-    if (mean > 16) return launch<Shape<OP, 64, 128, 64, 32, 64, 3>>(p, row_tile_bound(p, 64), stream);
-    return launch<Shape<OP, 16, 128, 16, 32, 64, 4>>(p, row_tile_bound(p, 16), stream);
+    if (mean > 128 && tile_count<Wide<OP>>(p) >= 2 * p.num_cu) return launch<Wide<OP>>(p, stream);
+    if (mean > 48) return launch<Middle<OP>>(p, stream);
+    if (is_small<OP>(p)) return launch<Small<OP>>(p, stream);
+    if (mean > 16) return launch<Low<OP>>(p, stream);
+    return launch<Few<OP>>(p, stream);
 }
 
 hipError_t launch_weight_grad(const GemmArgs& p, hipStream_t stream) {
-    using S = Shape<kWeightGrad, 256, 256, 128, 64, 64, 2, true>;
-    return launch<S>(p, (int64_t)p.E * ((p.M + S::BM - 1) / S::BM), stream);
+    if (tile_count<Wide<kWeightGrad>>(p) >= 4 * p.num_cu) return launch<Wide<kWeightGrad>>(p, stream);
+    return launch<Middle<kWeightGrad>>(p, stream);
+}
+
+hipError_t launch_after(const GemmArgs& rows, const GemmArgs& gate_up, const GemmArgs& down, hipStream_t stream) {
+    using R = Small<kRowGrad>;
+    using W = Middle<kWeightGrad>;
+    AfterArgs a{rows, gate_up, down, grid_of<R>(rows), grid_of<W>(gate_up)};
+    const int grid = a.grid_rows + a.grid_gate_up + grid_of<W>(down);
+    const size_t lds = R::lds(rows.E) > W::lds(rows.E) ? R::lds(rows.E) : W::lds(rows.E);
+    hipError_t e = allow_lds(ffn_after_kernel<R, W>, lds);
+    if (e != hipSuccess) return e;
+    ffn_after_kernel<R, W><<<grid, R::kThreads, lds, stream>>>(a);
+    return hipGetLastError();
 }
 
 GemmArgs rows_of(const FfnArgs& f) {
@@ -715,41 +782,37 @@ hipError_t launch_ffn_backward(const FfnArgs& f, hipStream_t stream) {
     hipError_t e = launch_rows<kActGrad>(p, stream);
     if (e != hipSuccess) return e;
     p.save = nullptr;
-    if (f.grad_pool) {
-        p.a = f.grad_gate_up;
-        p.a_ld = 2 * f.I;
-        p.b = f.w_gate_up;
-        p.b_ld = f.H;
-        p.b_expert = (int64_t)2 * f.I * f.H;
-        p.c = f.grad_pool;
-        p.N = f.H;
-        p.K = 2 * f.I;
-        e = launch_rows<kRowGrad>(p, stream);
-        if (e != hipSuccess) return e;
-    }
-    p.out_f32 = f.grad_f32;
-    p.accumulate = f.accumulate;
-    if (f.grad_w_gate_up) {
-        p.a = f.grad_gate_up;
-        p.a_ld = 2 * f.I;
-        p.b = f.pool;
-        p.b_ld = f.H;
-        p.c = f.grad_w_gate_up;
-        p.M = 2 * f.I;
-        p.N = f.H;
-        e = launch_weight_grad(p, stream);
-        if (e != hipSuccess) return e;
-    }
-    if (f.grad_w_down) {
-        p.a = f.grad_out;
-        p.a_ld = f.H;
-        p.b = f.act_rows;
-        p.b_ld = f.I;
-        p.c = f.grad_w_down;
-        p.M = f.H;
-        p.N = f.I;
-        e = launch_weight_grad(p, stream);
-    }
+    GemmArgs rows = p, gate_up = p, down = p;
+    rows.a = f.grad_gate_up;
+    rows.a_ld = 2 * f.I;
+    rows.b = f.w_gate_up;
+    rows.b_ld = f.H;
+    rows.b_expert = (int64_t)2 * f.I * f.H;
+    rows.c = f.grad_pool;
+    rows.N = f.H;
+    rows.K = 2 * f.I;
+    gate_up.a = f.grad_gate_up;
+    gate_up.a_ld = 2 * f.I;
+    gate_up.b = f.pool;
+    gate_up.b_ld = f.H;
+    gate_up.c = f.grad_w_gate_up;
+    gate_up.M = 2 * f.I;
+    gate_up.N = f.H;
+    down.a = f.grad_out;
+    down.a_ld = f.H;
+    down.b = f.act_rows;
+    down.b_ld = f.I;
+    down.c = f.grad_w_down;
+    down.M = f.H;
+    down.N = f.I;
+    gate_up.out_f32 = down.out_f32 = f.grad_f32;
+    gate_up.accumulate = down.accumulate = f.accumulate;
+    if (rows.c && gate_up.c && down.c && is_small<kRowGrad>(rows) &&
+        tile_count<Middle<kWeightGrad>>(gate_up) <= p.num_cu && tile_count<Middle<kWeightGrad>>(down) <= p.num_cu)
+        return launch_after(rows, gate_up, down, stream);
+    if (rows.c && (e = launch_rows<kRowGrad>(rows, stream)) != hipSuccess) return e;
+    if (gate_up.c && (e = launch_weight_grad(gate_up, stream)) != hipSuccess) return e;
+    if (down.c) e = launch_weight_grad(down, stream);
     return e;
 }
 
