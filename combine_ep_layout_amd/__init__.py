@@ -13,12 +13,17 @@ ep_layout, ep_dispatch, ep_combine, ...); ``EpHandle`` bundles them.
 from __future__ import annotations
 
 import ctypes
-import operator
 import os
 from typing import NamedTuple, Optional, Tuple
 
 import numpy as np
 import torch
+
+try:
+    from . import _ep_torch
+except ImportError as e:
+    raise ImportError("combine_ep_layout_amd/_ep_torch.so is missing or does not fit this torch: build it with "
+                      f"'python combine_ep_layout_amd/build.py' ({e})") from e
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libep_layout.so")
@@ -418,22 +423,27 @@ def route_backward(logits: torch.Tensor, topk_idx: torch.Tensor, grad_weights: t
     return grad_logits
 
 
-_attr = operator.attrgetter
+_GATHER_ERRORS = {1: (ValueError, "must have as many tensors as params"), 2: (TypeError, "must hold dense tensors"),
+                  3: (TypeError, "must be {dtype}"), 4: (ValueError, "must be on {device}"),
+                  5: (ValueError, "must be contiguous"),
+                  6: (ValueError, "has another number of values than its parameter needs")}
 
 
-def _column(tensors, dtype, sizes, device, name: str):
-    """Addresses of one kind of the step's tensors, checked.  A model has
-    hundreds: each check is one pass of a C function over the list."""
-    if len(tensors) != len(sizes):
-        raise ValueError(f"{name} must have {len(sizes)} tensors, got {len(tensors)}")
-    if list(map(torch.Tensor.numel, tensors)) != sizes:
-        raise ValueError(f"{name}: a tensor has another number of values than its parameter needs")
-    for key, want in ((_attr("dtype"), dtype), (_attr("device"), device), (torch.Tensor.is_contiguous, True)):
-        got = set(map(key, tensors))
-        if got != {want}:
-            what = "contiguous" if want is True else want
-            raise (TypeError if want is dtype else ValueError)(f"{name} must be {what}, got {got - {want}}")
-    return list(map(torch.Tensor.data_ptr, tensors))
+def _gather(table: np.ndarray, key: str, tensors, dtype, device: torch.device, per: int = 1) -> None:
+    """Checks one kind of the step's tensors and puts their addresses into the
+    table's column (per 0: their lengths into the column n)."""
+    base, offset = table.ctypes.data, table.dtype.fields[key][1]
+    if per == 0:
+        sizes = np.empty(len(table), np.int64)
+    else:
+        sizes = np.ascontiguousarray(table["n"])
+    wrong, which = _ep_torch.gather(tensors, dtype, device.index, sizes.ctypes.data, len(table), per, base + offset,
+                                    table.itemsize)
+    if wrong:
+        kind, text = _GATHER_ERRORS[wrong]
+        raise kind(f"{key}s, tensor {which}: " + text.format(dtype=dtype, device=device))
+    if per == 0:
+        table["n"] = sizes
 
 
 def adamw(params, grads, exp_avgs, exp_avg_sqs, step, lr: float = 1e-3, beta1: float = 0.9, beta2: float = 0.999,
@@ -461,20 +471,17 @@ def adamw(params, grads, exp_avgs, exp_avg_sqs, step, lr: float = 1e-3, beta1: f
     for dtype, name in ((p_dtype, "params"), (g_dtype, "grads")):
         if dtype not in (torch.float32, torch.bfloat16):
             raise TypeError(f"{name} must be float32 or bfloat16, got {dtype}")
-    sizes = list(map(torch.Tensor.numel, params))
     state = torch.uint8 if eight else torch.float32
     t = np.zeros(n, _ADAMW_TENSOR)
-    t["n"] = sizes
-    t["param"] = _column(params, p_dtype, sizes, device, "params")
-    t["grad"] = _column(grads, g_dtype, sizes, device, "grads")
-    t["exp_avg"] = _column(exp_avgs, state, sizes, device, "exp_avgs")
-    t["exp_avg_sq"] = _column(exp_avg_sqs, state, sizes, device, "exp_avg_sqs")
+    _gather(t, "param", params, p_dtype, device, per=0)
+    _gather(t, "grad", grads, g_dtype, device)
+    _gather(t, "exp_avg", exp_avgs, state, device)
+    _gather(t, "exp_avg_sq", exp_avg_sqs, state, device)
     if eight:
-        blocks = [(k + 127) // 128 for k in sizes]
-        t["exp_avg_scale"] = _column(exp_avg_scales, torch.float32, blocks, device, "exp_avg_scales")
-        t["exp_avg_sq_scale"] = _column(exp_avg_sq_scales, torch.float32, blocks, device, "exp_avg_sq_scales")
+        _gather(t, "exp_avg_scale", exp_avg_scales, torch.float32, device, per=128)
+        _gather(t, "exp_avg_sq_scale", exp_avg_sq_scales, torch.float32, device, per=128)
     if copies is not None:
-        t["copy"] = _column(copies, torch.bfloat16, sizes, device, "copies")
+        _gather(t, "copy", copies, torch.bfloat16, device)
     cfg = _AdamwConfig(lr=lr, beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay, grad_scale=1.0)
     cfg.flags = (EP_ADAMW_PARAM_BF16 if p_dtype == torch.bfloat16 else 0) | \
         (EP_ADAMW_GRAD_BF16 if g_dtype == torch.bfloat16 else 0) | (EP_ADAMW_STATE_8BIT if eight else 0)

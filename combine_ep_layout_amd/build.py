@@ -1,5 +1,6 @@
 """Build libep_layout.so (gfx950) in-tree with hipcc, and beside it
-libep_ceiling.so, the bandwidth probes the benchmark's ceiling leg loads.
+libep_ceiling.so, the bandwidth probes the benchmark's ceiling leg loads, and
+_ep_torch.so, the Python binding's helper for lists of tensors (host code).
 
     python combine_ep_layout_amd/build.py [-v] [-o OUT]
 
@@ -21,6 +22,8 @@ SOURCES = [os.path.join(CSRC, "ep_kernels.hip"), os.path.join(CSRC, "ep_api.hip"
            os.path.join(CSRC, "ep_route.hip"), os.path.join(CSRC, "ep_adamw.hip")]
 CEILING_LIB = os.path.join(PKG, "libep_ceiling.so")
 CEILING_SOURCES = [os.path.join(CSRC, "ep_ceiling.hip")]
+TORCH_LIB = os.path.join(PKG, "_ep_torch.so")
+TORCH_SOURCE = os.path.join(CSRC, "ep_torch.cpp")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
@@ -55,9 +58,26 @@ def _hipcc(out: str, sources: list, verbose: bool) -> str:
     return out
 
 
+def _torch_helper(verbose: bool) -> None:
+    import sysconfig
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = TORCH_LIB + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Wno-unknown-pragmas",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *(f"-isystem{d}" for d in (*include_paths(), sysconfig.get_paths()["include"])),
+           "-o", tmp, TORCH_SOURCE, f"-L{libs}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, TORCH_LIB)
+
+
 def build(verbose: bool = False, out: Optional[str] = None) -> str:
-    """Builds the library (to `out` if given) and the probe library; returns
-    the library's path."""
+    """Builds the library (to `out` if given), the probe library and the
+    binding's helper; returns the library's path."""
+    _torch_helper(verbose)
     _hipcc(CEILING_LIB, CEILING_SOURCES, verbose)
     return _hipcc(out or LIB, SOURCES, verbose)
 

@@ -59,6 +59,10 @@ __device__ __forceinline__ uint64_t ordered(double v) {
     return b >> 63 ? ~b : b | 0x8000000000000000ull;
 }
 
+__device__ __forceinline__ float unordered(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
     return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
@@ -79,11 +83,27 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
     v = max_step<0x143>(v);
     return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
-    return v;
+// The same moves for a sum (lanes without a source add 0, and always in the
+// same order) and for a maximum of floats above -inf.
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ float dpp_f32(float v) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, ROWS, 0xF, true));
 }
+__device__ __forceinline__ float last_lane(float v) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+    v += dpp_f32<0x111>(v);
+    v += dpp_f32<0x112>(v);
+    v += dpp_f32<0x114>(v);
+    v += dpp_f32<0x118>(v);
+    v += dpp_f32<0x142, 0xA>(v);        // into rows 1 and 3
+    v += dpp_f32<0x143, 0xC>(v);        // into rows 2 and 3
+    return last_lane(v);
+}
+// Maximum of floats that are no NaN, by their ordered keys.
+__device__ __forceinline__ float wave_max_f32(float v) { return unordered(wave_max(ordered(v))); }
+
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
 // Weights of the chosen experts, one a lane (lanes below K with an open
@@ -99,9 +119,7 @@ __device__ __forceinline__ float chosen_weight(const RouteArgs& a, bool on, floa
         if (total > 0x1p-60f) return s / total;
     }
     if (!a.sigmoid && !a.normalize) return on ? expf(l - top) / sum : 0.0f;
-    float m = on ? l : -__builtin_inff();
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+    const float m = wave_max_f32(on ? l : -__builtin_inff());
     const float e = on ? expf(l - m) : 0.0f;
     const float total = wave_sum(e);
     return on ? e / total : 0.0f;
@@ -113,8 +131,7 @@ __device__ __forceinline__ void row_softmax(const float (&l)[N], float& top, flo
     top = -__builtin_inff();
 #pragma unroll
     for (int i = 0; i < N; ++i) top = fmaxf(top, l[i]);
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+    top = wave_max_f32(top);
     sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; ++i) sum += l[i] > -__builtin_inff() ? expf(l[i] - top) : 0.0f;
@@ -157,38 +174,46 @@ route_kernel(RouteArgs a) {
     int mine = -1;              // lane k: the k-th chosen expert and its logit
     float mine_l = 0.0f;
     for (int k = 0; k < a.K; ++k) {
+        // the lane's best expert left: its key, slot and (BIASED) logit
         uint32_t best = 0, best_lo = 0;
+        int slot = 0;
+        float best_l = 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
+            bool more = hi[i] > best;
+            if constexpr (BIASED) more = more || (hi[i] == best && lo[i] > best_lo);
+            best = more ? hi[i] : best;
+            slot = more ? i : slot;
             if constexpr (BIASED) {
-                const bool more = hi[i] > best || (hi[i] == best && lo[i] > best_lo);
-                best = more ? hi[i] : best;
                 best_lo = more ? lo[i] : best_lo;
-            } else {
-                best = hi[i] > best ? hi[i] : best;
+                best_l = more ? l[i] : best_l;
             }
         }
         const uint32_t win = wave_max(best);
         if (win == 0) break;                    // no expert is left
-        uint32_t win_lo = 0;
-        if constexpr (BIASED) win_lo = wave_max(best == win ? best_lo : 0u);
-        // the lowest expert that has this key: the lowest slot, then the lowest lane
-        int e = -1;
-        float le = 0.0f;
+        bool is = best == win;
+        if constexpr (BIASED) {
+            const uint32_t win_lo = wave_max(is ? best_lo : 0u);        // every lane takes part
+            is = is && best_lo == win_lo;
+        }
+        // the lowest expert of those that have the key; mostly there is one
+        const uint64_t who = __ballot(is);
+        int e;
+        if ((who & (who - 1)) == 0) {
+            const int owner = __builtin_ctzll(who);
+            e = __builtin_amdgcn_readlane(slot, owner) * kWave + owner;
+        } else {
+            e = 0xFFFF - (int)wave_max(is ? 0xFFFFu - (uint32_t)(slot * kWave + lane) : 0u);
+        }
+        float le = unordered(win);
+        if constexpr (BIASED)
+            le = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(best_l), e & (kWave - 1)));
+        const bool owner = lane == (e & (kWave - 1));
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            bool is = hi[i] == win;
-            if constexpr (BIASED) is = is && lo[i] == win_lo;
-            const uint64_t who = __ballot(is);
-            if (e < 0 && who) {
-                const int owner = __builtin_ctzll(who);
-                e = i * kWave + owner;
-                le = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(l[i]), owner));
-                if (lane == owner) {
-                    hi[i] = 0;
-                    if constexpr (BIASED) lo[i] = 0;
-                }
-            }
+            const bool taken = owner && i == slot;
+            hi[i] = taken ? 0u : hi[i];
+            if constexpr (BIASED) lo[i] = taken ? 0u : lo[i];
         }
         if (lane == k) {
             mine = e;

@@ -27,6 +27,11 @@ SHAPES = [
     (700, 2, 5, 4096, 128, 128, "skewed"),
     (1000, 1, 1024, 1, 64, 48, "skewed"),      # most experts without a row
     (40, 32, 40, 16, 128, 64, "uniform"),      # every expert of every token
+    # two rounds of tiles: the widest shape in every product
+    (2400, 4, 64, 16, 1288, 648, "uniform"),
+    (2400, 4, 64, 100, 1288, 648, "skewed"),
+    # few rows, more tiles than compute units: 64 x 128 tiles
+    (1280, 2, 128, 16, 400, 400, "uniform"),
 ]
 
 
