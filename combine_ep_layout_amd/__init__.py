@@ -182,8 +182,10 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(stream) -> ctypes.c_void_p:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    # the raw handle: torch.cuda.current_stream() makes a Stream object for 2.7 us
+    if stream is None:
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    return ctypes.c_void_p(stream.cuda_stream)
 
 
 def _used_on(stream, *tensors) -> None:
@@ -358,16 +360,24 @@ def ep_handle_sync_status(h, stream=None) -> int:
 
 def _route_args(logits: torch.Tensor, score: str, normalize: bool) -> int:
     """Checks a router's logits; returns the call's flags."""
-    if score not in SCORES:
-        raise ValueError(f"score must be one of {sorted(SCORES)}")
-    if logits.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    dtype = logits.dtype
+    if dtype is torch.float32:
+        flags = 0
+    elif dtype is torch.bfloat16:
+        flags = EP_ROUTE_BF16
+    else:
+        raise TypeError(f"logits must be float32 or bfloat16, got {dtype}")
     if not logits.is_cuda:
         raise ValueError(f"logits must be on a GPU, got {logits.device}")
-    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1) or _row_stride(logits) < logits.shape[1]:
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {sorted(SCORES)}")
+    if logits.dim() != 2 or not _plain_rows(logits):
         raise ValueError("logits must be [num_tokens, num_experts] with contiguous rows that do not overlap")
-    return SCORES[score] | (EP_ROUTE_NORMALIZE if normalize else 0) | \
-        (EP_ROUTE_BF16 if logits.dtype == torch.bfloat16 else 0)
+    return flags | SCORES[score] | (EP_ROUTE_NORMALIZE if normalize else 0)
+
+
+def _plain_rows(t: torch.Tensor) -> bool:
+    return t.is_contiguous() or ((t.shape[1] == 1 or t.stride(1) == 1) and _row_stride(t) >= t.shape[1])
 
 
 def _row_stride(t: torch.Tensor) -> int:
@@ -384,17 +394,21 @@ def route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: Option
     Equal scores: the lowest expert first.  -inf closes an expert; slots without
     an expert get -1 and weight 0 (masked for layout())."""
     flags = _route_args(logits, score, normalize)
+    device = logits.device
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return route(logits, top_k, score, bias, normalize, scale, stream)
     T, E = logits.shape
     if bias is not None:
-        _require(bias, torch.float32, "bias", logits.device)
+        _require(bias, torch.float32, "bias", device)
         if tuple(bias.shape) != (E,):
             raise ValueError(f"bias must be [{E}]")
-    with torch.cuda.device(logits.device):
-        idx = torch.empty(T, top_k, dtype=torch.int32, device=logits.device)
-        w = torch.empty(T, top_k, dtype=torch.float32, device=logits.device)
-        _check(_lib.ep_route(_ptr(logits), _row_stride(logits), T, E, top_k, flags, _ptr(bias), scale, _ptr(idx),
-                             _ptr(w), _stream(stream)), "ep_route")
-        _used_on(stream, idx, w)
+    idx = torch.empty((T, top_k), dtype=torch.int32, device=device)
+    w = torch.empty((T, top_k), dtype=torch.float32, device=device)
+    _check(_lib.ep_route(logits.data_ptr(), _row_stride(logits), T, E, top_k, flags,
+                         None if bias is None else bias.data_ptr(), scale, idx.data_ptr(), w.data_ptr(),
+                         _stream(stream)), "ep_route")
+    _used_on(stream, idx, w)
     return idx, w
 
 
@@ -404,22 +418,24 @@ def route_backward(logits: torch.Tensor, topk_idx: torch.Tensor, grad_weights: t
     """Backward of route: the logits' gradient, in their type, from that of the
     weights (combine_backward()'s grad_weights)."""
     flags = _route_args(logits, score, normalize)
+    device = logits.device
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return route_backward(logits, topk_idx, grad_weights, score, normalize, scale, grad_logits, stream)
     T, E = logits.shape
-    _require(topk_idx, torch.int32, "topk_idx", logits.device)
-    _require(grad_weights, torch.float32, "grad_weights", logits.device)
+    _require(topk_idx, torch.int32, "topk_idx", device)
+    _require(grad_weights, torch.float32, "grad_weights", device)
     if topk_idx.dim() != 2 or topk_idx.shape[0] != T or grad_weights.shape != topk_idx.shape:
         raise ValueError("topk_idx / grad_weights must both be [num_tokens, top_k]")
-    with torch.cuda.device(logits.device):
-        if grad_logits is None:
-            grad_logits = torch.empty(T, E, dtype=logits.dtype, device=logits.device)
-        if grad_logits.dtype != logits.dtype or grad_logits.device != logits.device or \
-                grad_logits.shape != logits.shape or (E > 1 and grad_logits.stride(1) != 1) or \
-                _row_stride(grad_logits) < E:
-            raise ValueError("grad_logits must be like logits")
-        _check(_lib.ep_route_backward(_ptr(logits), _row_stride(logits), T, E, topk_idx.shape[1], flags, scale,
-                                      _ptr(topk_idx), _ptr(grad_weights), _ptr(grad_logits),
-                                      _row_stride(grad_logits), _stream(stream)), "ep_route_backward")
-        _used_on(stream, grad_logits)
+    if grad_logits is None:
+        grad_logits = torch.empty((T, E), dtype=logits.dtype, device=device)
+    elif grad_logits.dtype != logits.dtype or grad_logits.device != device or grad_logits.shape != logits.shape or \
+            not _plain_rows(grad_logits):
+        raise ValueError("grad_logits must be like logits")
+    _check(_lib.ep_route_backward(logits.data_ptr(), _row_stride(logits), T, E, topk_idx.shape[1], flags, scale,
+                                  topk_idx.data_ptr(), grad_weights.data_ptr(), grad_logits.data_ptr(),
+                                  _row_stride(grad_logits), _stream(stream)), "ep_route_backward")
+    _used_on(stream, grad_logits)
     return grad_logits
 
 
