@@ -10,7 +10,7 @@ resident in HBM when the timed region starts.
     python bench.py [--gpus 1] [--steps K] [--warmup W] [--config NAME]
                     [--no-cpu-baseline] [--copy-calibration]
                     [--borrow-compare | --backward | --gate | --fp8-variants | --graph | --ceiling
-                     | --overlap]
+                     | --overlap | --layer]
 
 Prints one JSON line.  "value" is algorithmic bytes moved per step / step
 time, over exactly K steps with nothing else on the stream.  Per-kernel times
@@ -277,6 +277,88 @@ def backward_bench(cfg, steps: int, warmup: int) -> dict:
             "gbs": {"combine_backward": round(b_cb / (cb * 1e-6) / 1e9, 1),
                     "dispatch_backward": round(b_db / (db * 1e-6) / 1e9, 1)},
             "pct_of_peak": round(100.0 * (b_cb + b_db) / ((cb + db) * 1e-6) / 1e9 / PEAK_GBS, 2)}
+
+
+LAYER_INTER = 2048      # the experts' intermediate size in the layer measurement
+
+
+def layer_bench(cfg, steps: int, warmup: int) -> dict:
+    """Times a training step of a whole MoE layer of the workload's tokens and
+    experts (all of them here: the router picks the top_k itself): route,
+    layout, dispatch, the experts' feed-forward, combine, their backward calls
+    back to the logits, and the AdamW step on the experts' weights (float32
+    masters, bf16 gradients and working copies, states in 8 bits)."""
+    import torch
+    import combine_ep_layout_amd as ep
+    dev = torch.device("cuda", 0)
+    stream = torch.cuda.current_stream()
+    T, K, H, E, I = cfg.tokens, cfg.top_k, cfg.hidden, cfg.num_experts, LAYER_INTER
+    g = torch.Generator(device=dev)
+    g.manual_seed(0)
+    bf16 = torch.bfloat16
+    normal = lambda *s, std=1.0, dtype=bf16: torch.empty(s, dtype=dtype, device=dev).normal_(0, std, generator=g)
+    x, grad_y = normal(T, H), normal(T, H)
+    logits = normal(T, E, dtype=torch.float32)
+    copies = [normal(E, 2 * I, H, std=H ** -0.5), normal(E, H, I, std=I ** -0.5)]
+    masters = [c.float() for c in copies]
+    grads = [torch.empty_like(c) for c in copies]
+    state = lambda: ([torch.zeros(m.shape, dtype=torch.uint8, device=dev) for m in masters],
+                     [torch.zeros(m.numel() // 128, device=dev) for m in masters])
+    (m, ms), (v, vs) = state(), state()
+    h = ep.EpHandle(T, K, E, cfg.block_m)
+    cap = h.capacity_rows
+    pool, _ = h.new_pool(H)
+    out, geo, gp, act = torch.empty_like(pool), torch.empty_like(pool), torch.empty_like(pool), normal(cap, I)
+    gate_up, ggu = torch.empty(cap, 2 * I, device=dev), torch.empty(cap, 2 * I, dtype=bf16, device=dev)
+    saved = ep.FfnSaved(act, gate_up)
+    s = {}
+
+    def forward_route():
+        s["idx"], s["w"] = ep.route(logits, K)
+
+    def forward_dispatch():
+        s["epoch"] = h.layout(s["idx"], s["w"])
+        h.dispatch(x, pool)
+
+    def backward_ffn():
+        h.expert_ffn_backward(s["epoch"], geo, pool, *copies, saved, grad_pool=gp, grad_gate_up=ggu,
+                              grad_w_gate_up=grads[0], grad_w_down=grads[1])
+
+    def backward_combine():
+        s["gw"] = h.combine_backward(s["epoch"], grad_y, out, geo)[1]
+
+    legs = [("route", forward_route), ("layout_dispatch", forward_dispatch),
+            ("expert_ffn", lambda: h.expert_ffn(s["epoch"], pool, *copies, out=out, act=act, gate_up=gate_up, save=True)),
+            ("combine", lambda: h.combine(s["epoch"], out)), ("combine_backward", backward_combine),
+            ("expert_ffn_backward", backward_ffn), ("dispatch_backward", lambda: h.dispatch_backward(s["epoch"], gp)),
+            ("route_backward", lambda: ep.route_backward(logits, s["idx"], s["gw"])),
+            ("adamw", lambda: ep.adamw(masters, grads, m, v, step=1, exp_avg_scales=ms, exp_avg_sq_scales=vs,
+                                       copies=copies))]
+    for _ in range(warmup):
+        for _, f in legs:
+            f()
+    torch.cuda.synchronize()
+    ev = [[torch.cuda.Event(enable_timing=True) for _ in range(len(legs) + 1)] for _ in range(steps)]
+    t0 = time.perf_counter()
+    for e in ev:
+        e[0].record(stream)
+        for i, (_, f) in enumerate(legs):
+            f()
+            e[i + 1].record(stream)
+    torch.cuda.synchronize()
+    step = (time.perf_counter() - t0) / steps
+    us = {name: round(float(np.mean([e[i].elapsed_time(e[i + 1]) for e in ev])) * 1e3, 1) for i, (name, _) in enumerate(legs)}
+    assert h.sync_status() == ep.EP_OK
+    h.close()
+    rows, n = T * K, sum(t.numel() for t in masters)
+    return {"metric": "MoE layer training step, tokens/s", "unit": "tokens/s", "value": round(T / step, 1),
+            "higher_is_better": True, "ms_per_step": round(step * 1e3, 3), "data": "synthetic", "dtype": "bf16",
+            "config": {"workload": f"{cfg.name}: {T} tokens, hidden {H}, {E} experts of intermediate size {I}, top-{K} of "
+                                   f"random logits, BLOCK_M {cfg.block_m}; AdamW with 8-bit states on {n} values"},
+            "legs_us": us,
+            "tflops": {"expert_ffn": round(6e-6 * rows * H * I / us["expert_ffn"], 1),
+                       "expert_ffn_backward": round(12e-6 * rows * H * I / us["expert_ffn_backward"], 1)},
+            "gbs": {"adamw": round(n * (16 + 16 / 128) / us["adamw"] * 1e-3, 1)}}
 
 
 def _time_us(fn, steps: int, warmup: int, stream) -> float:
@@ -780,6 +862,9 @@ def main() -> int:
                     help="print the borrowed-view vs copy comparison instead")
     ap.add_argument("--backward", action="store_true",
                     help="print the backward (combine_grads + dispatch_grads) measurement instead")
+    ap.add_argument("--layer", action="store_true",
+                    help="print the training step of a whole layer (router, dispatch, experts, combine, "
+                         "backward, AdamW) instead")
     ap.add_argument("--gate", action="store_true",
                     help="print the per-token combine gate measurement instead")
     ap.add_argument("--fp8-variants", action="store_true",
@@ -830,6 +915,10 @@ def main() -> int:
     if args.backward:
         torch.cuda.set_device(0)
         print(json.dumps(backward_bench(CONFIGS[args.config], args.steps, args.warmup)), flush=True)
+        return 0
+    if args.layer:
+        torch.cuda.set_device(0)
+        print(json.dumps(layer_bench(CONFIGS[args.config], args.steps, args.warmup)), flush=True)
         return 0
     if args.gate:
         torch.cuda.set_device(0)
