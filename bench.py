@@ -66,15 +66,17 @@ def algorithmic_bytes(cfg, idx: np.ndarray, counts: np.ndarray, fp8: bool):
                                                           // cfg.block_m).sum() * cfg.block_m)}
 
 
+# the sources of dispatch and combine, which the counters were taken on
+PATH_SOURCES = ("ep_api.hip", "ep_internal.h", "ep_kernels.hip", "ep_noalloc.hip")
+
+
 def kernel_source_sha() -> str:
-    """Hash of the library sources with comments and blank space removed, so
+    """Hash of the path's sources with comments and blank space removed, so
     that a comment edit does not orphan counters taken on the same code."""
     import re
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "combine_ep_layout_amd", "csrc")
-    for name in sorted(os.listdir(csrc)):
-        if name == "ep_ceiling.hip":                    # the bandwidth probes, not the path
-            continue
+    for name in PATH_SOURCES:
         with open(os.path.join(csrc, name), encoding="utf-8") as f:
             text = f.read()
         text = re.sub(r"/\*.*?\*/", " ", text, flags=re.S)

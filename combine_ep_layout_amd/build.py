@@ -17,7 +17,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libep_layout.so")
-SOURCES = [os.path.join(CSRC, "ep_kernels.hip"), os.path.join(CSRC, "ep_api.hip"),
+SOURCES = [os.path.join(CSRC, "ep_kernels.hip"), os.path.join(CSRC, "ep_expert_api.hip"),
            os.path.join(CSRC, "ep_noalloc.hip"), os.path.join(CSRC, "ep_ffn.hip"),
            os.path.join(CSRC, "ep_route.hip"), os.path.join(CSRC, "ep_adamw.hip")]
 CEILING_LIB = os.path.join(PKG, "libep_ceiling.so")

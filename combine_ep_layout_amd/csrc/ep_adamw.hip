@@ -307,8 +307,8 @@ extern "C" ep_status ep_adamw(const ep_adamw_tensor* tensors, int32_t count, con
         return EP_ERR_INVALID_ARGUMENT;
     const bool eight = cfg->flags & EP_ADAMW_STATE_8BIT, pb = cfg->flags & EP_ADAMW_PARAM_BF16;
     const int64_t ps = pb ? 2 : 4, gs = (cfg->flags & EP_ADAMW_GRAD_BF16) ? 2 : 4, ss = eight ? 1 : 4;
-    // the count of a launch's workgroups stays far below 2^31
-    constexpr int64_t kMost = (int64_t)1 << 40;
+    // a launch's grid stays below 2^32 threads
+    constexpr int64_t kMostChunks = (int64_t)1 << 23, kMost = kMostChunks * kChunk;
     try {
         std::vector<Range> ranges;
         ranges.reserve((size_t)count * 7);
@@ -368,7 +368,7 @@ extern "C" ep_status ep_adamw(const ep_adamw_tensor* tensors, int32_t count, con
             const ep_adamw_tensor& t = tensors[i];
             if (t.n == 0) continue;
             const int64_t c = (t.n + kChunk - 1) / kChunk;
-            if (a.count > 0 && chunks + c > (1 << 30)) break;
+            if (a.count > 0 && chunks + c > kMostChunks) break;
             a.first[a.count] = (int32_t)chunks;
             a.t[a.count++] = {t.param, t.grad, t.exp_avg, t.exp_avg_sq, t.exp_avg_scale, t.exp_avg_sq_scale, t.copy, t.n};
             chunks += c;

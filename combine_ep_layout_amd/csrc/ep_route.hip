@@ -21,6 +21,7 @@ constexpr int kWave = 64;
 constexpr int kRouteWaves = 4;              // tokens of a workgroup
 constexpr int kRouteMaxExperts = 1024;
 constexpr int kRouteMaxTopK = 32;
+constexpr int kRouteMaxTokens = 1 << 25;    // a wave each: the grid stays below 2^32 threads
 
 struct RouteArgs {
     const void* logits;         // [T, ld] fp32 or bf16
@@ -308,7 +309,7 @@ ep_status check_route(const void* logits, int64_t ld, int32_t T, int32_t E, int3
                       float scale, RouteArgs& a) {
     if (flags & ~kRouteFlags) return EP_ERR_INVALID_ARGUMENT;
     if (T < 0 || E < 1 || K < 1 || K > E || ld < E || scale != scale) return EP_ERR_INVALID_ARGUMENT;
-    if (E > kRouteMaxExperts || K > kRouteMaxTopK) return EP_ERR_UNSUPPORTED;
+    if (E > kRouteMaxExperts || K > kRouteMaxTopK || T > kRouteMaxTokens) return EP_ERR_UNSUPPORTED;
     if (T > 0 && (!logits || !aligned(logits, (flags & EP_ROUTE_BF16) ? 2 : 4))) return EP_ERR_INVALID_ARGUMENT;
     a.logits = logits;
     a.ld = ld;

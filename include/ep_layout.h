@@ -50,7 +50,8 @@
  *   - Arrays: x, pool, expert_out and y are row-major; bf16 values are passed
  *     as their 16-bit patterns.
  *   - HIP graph capture: ep_layout, ep_dispatch, ep_combine, ep_combine_gated,
- *     the backward calls and ep_fp8_cast_back only launch kernels (nothing is
+ *     the backward calls, ep_fp8_cast_back, ep_route, ep_expert_ffn, their
+ *     backward calls and ep_adamw only launch kernels (nothing is
  *     allocated and no memory is set through the runtime), so they can be
  *     captured and replayed.  The host-side counters advance when a call is
  *     captured, not when it is replayed: a replay repeats the captured epoch,
@@ -171,10 +172,11 @@ int32_t ep_num_tokens(const ep_handle* h);
 int64_t ep_scale_ld(const ep_handle* h);
 
 /* The router before ep_layout: each token's top_k experts and their weights
- * from its logits.  Needs no handle.
+ * from its logits.  Needs no handle; the buffers are on the current device.
  *   logits        device fp32 (EP_ROUTE_BF16: bf16) [num_tokens, num_experts],
  *                 rows logits_ld >= num_experts values apart.
- *   num_experts   1..1024; top_k 1..32, at most num_experts.
+ *   num_tokens    0..2^25; num_experts 1..1024; top_k 1..32, at most num_experts
+ *                 (more is EP_ERR_UNSUPPORTED).
  *   flags         scores are the softmax over all experts of the token, with
  *                 EP_ROUTE_SIGMOID 1 / (1 + exp(-logit)); EP_ROUTE_NORMALIZE
  *                 divides a token's weights by their sum.
@@ -399,7 +401,8 @@ ep_status ep_dispatch_backward(const ep_handle* h, uint32_t epoch, const void* g
  *               may be the pool itself, otherwise no buffer that is written
  *               may share memory with another (EP_ERR_INVALID_ARGUMENT).
  * hidden % 8 == 0, inter % 8 == 0; hidden * inter above 2^29, or either above
- * 65536, is EP_ERR_UNSUPPORTED.  Sums are fp32; a and out are each rounded
+ * 65536, is EP_ERR_UNSUPPORTED, another current device than the handle's
+ * EP_ERR_INVALID_ARGUMENT.  Sums are fp32; a and out are each rounded
  * once, to nearest even.  Only real rows are read and written: rows past an
  * expert's last keep what they hold, in every buffer.  The result depends on
  * the rows alone, never on timing.  Two launches; capturable. */
@@ -443,7 +446,8 @@ ep_status ep_expert_ffn_backward(const ep_handle* h, uint32_t epoch, const void*
  *     m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
  *     p = p (1 - lr weight_decay)
  *         - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
- * in fp32, each result rounded once.  Needs no handle.
+ * in fp32, each result rounded once.  Needs no handle; the buffers are on the
+ * current device.
  *   tensors   host array of `count` entries; read before the call returns.
  *     param        device fp32 (EP_ADAMW_PARAM_BF16: bf16) [n], updated.
  *     grad         device fp32 (EP_ADAMW_GRAD_BF16: bf16) [n].
@@ -457,7 +461,8 @@ ep_status ep_expert_ffn_backward(const ep_handle* h, uint32_t epoch, const void*
  *                  EP_ADAMW_STATE_8BIT, else NULL.
  *     copy         device bf16 [n] or NULL: receives the updated fp32 parameter
  *                  rounded (with fp32 parameters only, else EP_ERR_UNSUPPORTED).
- *     n            >= 0, any.  Buffers are 16-byte aligned, scales 4-byte.
+ *     n            0..2^34 (more is EP_ERR_UNSUPPORTED).  Buffers are 16-byte
+ *                  aligned, scales 4-byte.
  *   cfg       host.  step >= 1, or step_dev (device int64, read when the step
  *             runs: a replayed graph takes the value it then holds; 8-byte
  *             aligned) instead; grad_scale_dev (device fp32 or NULL) is a further

@@ -39,7 +39,7 @@ def test_route_refusals(ep):
                 dict(logits=None), dict(logits=A[0] + 2), dict(flags=ep.EP_ROUTE_BF16, logits=A[0] + 1), dict(idx=None),
                 dict(w=None), dict(idx=A[1] + 2), dict(flags=ep.EP_ROUTE_SIGMOID, bias=A[3] + 1)):
         assert call(**bad) == INV, bad
-    for bad in (dict(E=1025, ld=1025), dict(E=64, ld=64, K=33), dict(bias=A[3])):
+    for bad in (dict(E=1025, ld=1025), dict(E=64, ld=64, K=33), dict(bias=A[3]), dict(T=(1 << 25) + 1)):
         assert call(**bad) == UNS, bad
 
 
@@ -83,7 +83,7 @@ def test_adamw_refusals(ep):
     assert adamw(ep, [ok, {**ok, "param": A[5], "exp_avg": A[6], "exp_avg_sq": A[0] + 384}]) == INV     # across tensors
     assert adamw(ep, [ok, none, ok]) == INV                                                             # twice
     assert adamw(ep, [{**ok, "copy": A[4]}], ep.EP_ADAMW_PARAM_BF16) == UNS
-    assert adamw(ep, [{**ok, "n": 1 << 50}]) == UNS
+    assert adamw(ep, [{**ok, "n": 1 << 50}]) == UNS and adamw(ep, [{**ok, "n": (1 << 34) + 1}]) == UNS
     eight = {**ok, "exp_avg_scale": A[4], "exp_avg_sq_scale": A[5]}
     for bad in (dict(exp_avg_scale=0), dict(exp_avg_sq_scale=0), dict(exp_avg_scale=A[4] + 2), dict(exp_avg_scale=A[5])):
         assert adamw(ep, [{**eight, **bad}], ep.EP_ADAMW_STATE_8BIT) == INV, bad
