@@ -5,8 +5,9 @@
 //     m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2
 //     p = p (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps)
 // The states are fp32, or 8 bits: e4m3fn codes of m and of sqrt(v) with one
-// fp32 scale for each 128 values, the codes and scales of the FP8 dispatch's
-// float32 flavour.  The root is stored because its range is half of v's in
+// fp32 scale for each 128 values, which the FP8 dispatch's float32 flavour reads:
+// with a the block's largest magnitude, scale a * (1/448) and codes of
+// x * ((1/a) * 448), one rounded reciprocal instead of two quotients.  The root is stored because its range is half of v's in
 // the exponent, which e4m3 spans within a block; a root above zero keeps the
 // least code rather than becoming zero, so no step is divided by eps alone.
 //
@@ -113,7 +114,7 @@ __device__ __forceinline__ float update(const Scalars& s, float p, float g, floa
     g *= s.grad_scale;
     m = s.beta1 * m + s.rest1 * g;
     v = s.beta2 * v + s.rest2 * (g * g);
-    r = __fsqrt_rn(v);
+    r = sqrtf(v);               // correctly rounded, as the quotients are: codes next to a tie depend on it
     return p * s.decay - s.step_size * (m / (r / s.root_bc2 + s.eps));
 }
 
@@ -171,8 +172,8 @@ __device__ __forceinline__ float max32(float v) {        // over the 32 lanes of
 __device__ __forceinline__ uint32_t encode4(const float (&x)[4], float& scale) {
     float top = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
     top = fmaxf(max32(top), 448.0f * 0x1p-126f);
-    scale = top / 448.0f;
-    const float f = 448.0f / top;
+    scale = top * (1.0f / 448.0f);
+    const float f = (1.0f / top) * 448.0f;
     int w = __builtin_amdgcn_cvt_pk_fp8_f32(x[0] * f, x[1] * f, 0, false);
     w = __builtin_amdgcn_cvt_pk_fp8_f32(x[2] * f, x[3] * f, w, true);
     return (uint32_t)w;

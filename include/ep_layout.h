@@ -452,10 +452,13 @@ ep_status ep_expert_ffn_backward(const ep_handle* h, uint32_t epoch, const void*
  *     param        device fp32 (EP_ADAMW_PARAM_BF16: bf16) [n], updated.
  *     grad         device fp32 (EP_ADAMW_GRAD_BF16: bf16) [n].
  *     exp_avg, exp_avg_sq   device fp32 [n]: m and v, updated.  With
- *                  EP_ADAMW_STATE_8BIT e4m3fn bytes [n] of m and of sqrt(v), in
- *                  the float32 scale flavour of the FP8 dispatch
- *                  (EP_SCALE_F32) over each 128 values in order, the last
- *                  block possibly shorter; a root above zero never gets code 0.
+ *                  EP_ADAMW_STATE_8BIT e4m3fn bytes [n] of m and of sqrt(v), with
+ *                  a float32 scale for each 128 values in order (the last
+ *                  block possibly shorter), as ep_fp8_cast_back reads them with
+ *                  EP_SCALE_F32: for the largest magnitude a of the block (at
+ *                  least 448*2^-126; NaN takes no part) the scale is
+ *                  a * (1/448) and the codes are x * ((1/a) * 448) to nearest
+ *                  even, each step in fp32; a root above zero never gets code 0.
  *                  An infinity makes its block of 128 NaN, as one scale holds it.
  *     exp_avg_scale, exp_avg_sq_scale   device fp32 [ceil(n / 128)] with
  *                  EP_ADAMW_STATE_8BIT, else NULL.

@@ -10,7 +10,9 @@ pytestmark = pytest.mark.gpu
 
 NEG = float("-inf")
 SHAPES = [(1, 1, 1), (1, 8, 8), (3, 2, 1), (5, 63, 7), (4, 64, 32), (129, 65, 2), (64, 128, 6), (33, 200, 8), (16, 256, 8),
-          (7, 257, 9), (9, 500, 1), (6, 513, 32), (5, 1023, 10), (17, 1024, 16)]
+          (7, 257, 9), (9, 500, 1), (6, 513, 32), (5, 1023, 10), (17, 1024, 16),
+          # many tokens, four a wave; then many that do not take that form
+          (8193, 3, 2), (8200, 64, 16), (9003, 100, 7), (8199, 256, 8), (8194, 129, 1), (8193, 256, 17), (8193, 300, 8)]
 FORMS = [("softmax", True, False), ("softmax", False, False), ("sigmoid", True, False), ("sigmoid", False, True),
          ("sigmoid", True, True)]
 
@@ -136,7 +138,7 @@ def test_bias_chooses_but_does_not_weigh():
 
 def test_strided_rows_and_many_tokens():
     import combine_ep_layout_amd as ep
-    wide = torch.randn(5001, 100, device=dev())
+    wide = torch.randn(9001, 100, device=dev())
     l = wide[:, 10:43]
     idx, w = ep.route(l, 4)
     a, b = ep.route(l.contiguous(), 4)

@@ -17,7 +17,8 @@ HYPER = dict(lr=3e-3, beta1=0.9, beta2=0.99, eps=1e-8, weight_decay=0.05)
 
 
 def encode(x):
-    """The f32 flavour of the FP8 dispatch: codes and scales of each 128 values (fp32 arithmetic, as it is defined)."""
+    """Codes and scales of each 128 values, in the fp32 operations of the definition (torch's quotient of a number by a
+    tensor is the number times the reciprocal, and its quotient by a number the product with that number's reciprocal)."""
     n = x.numel()
     b = torch.zeros((n + 127) // 128 * 128, device=x.device)
     b[:n] = x
@@ -121,6 +122,29 @@ def test_step(p_dtype, g_dtype, copy, eight):
         before = clone(s)
         ep.adamw(**s, step=step, **HYPER)
         check(s, before, step)
+
+
+def test_codes_are_those_of_the_definition():
+    """Bit for bit over some 30 million values: one code off by one would show here, and in every later step."""
+    import combine_ep_layout_amd as ep
+    h = HYPER
+    for seed in range(3):
+        s = make([5_000_000, 77], F32, BF16, True, False, seed=seed)
+        before = clone(s)
+        ep.adamw(**s, step=9, **HYPER)
+        for i in range(2):
+            g = before["grads"][i].float()
+            value = lambda k, t: (before[k][i].view(torch.float8_e4m3fn).float() *
+                                  before[t][i].repeat_interleave(128)[: g.numel()])
+            m = h["beta1"] * value("exp_avgs", "exp_avg_scales") + (1 - h["beta1"]) * g
+            v = h["beta2"] * value("exp_avg_sqs", "exp_avg_sq_scales").square() + (1 - h["beta2"]) * (g * g)
+            root = torch.sqrt(v)
+            codes, scales = encode(m)
+            assert torch.equal(s["exp_avg_scales"][i], scales)
+            assert torch.equal(s["exp_avgs"][i], codes)
+            codes, scales = encode(root)
+            assert torch.equal(s["exp_avg_sq_scales"][i], scales)
+            assert torch.equal(s["exp_avg_sqs"][i], torch.where((codes == 0) & (root > 0), torch.ones_like(codes), codes))
 
 
 def test_more_tensors_than_a_launch_and_lists_of_one():
