@@ -18,7 +18,17 @@
 // fragment is one ds_read_b128; where it is not, the tile keeps the memory's
 // order and two transposing reads (ds_read_b64_tr_b16) make the fragment, so
 // no operand is transposed in memory.  Both layouts are swizzled by permuting
-// which 16 bytes a lane fetches, since the load itself fills LDS linearly.
+// which 16 bytes a lane fetches, since the load itself fills LDS linearly (no
+// bank conflicts are counted).
+//
+// What bounds it, measured on MI355X at 32 experts of 2048 rows, 7168 x 2048:
+// a 256 x 256 tile's matrix instructions alone run at 1.95 PFLOP/s, at the 2.1
+// GHz that their power leaves, with the LDS reads at 1.64-1.76; the loads alone
+// (64 KiB for 64 summed indices) keep pace with 1.95-2.1, which is 16 TB/s out
+// of L2, 26 bytes a cycle for each compute unit.  Together, at 1.9 GHz, they
+// reach 1.04 (gradient of the activation) to 1.29 PFLOP/s (gate and up): both
+// need most of the time, and two tiles in LDS hide only part of a load's
+// latency.  Few rows are bound by the weights' bytes instead: 5.7-5.8 TB/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include <utility>
@@ -36,7 +46,9 @@ typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) char lds_char;
 
 constexpr int kWave = 64;
-constexpr uint32_t kOutOfRange = 0x80000000u;   // offset past every buffer's range: such a lane loads zeros
+// Offset past every buffer's range, also with a tile's own offset added: such a
+// lane loads zeros.
+constexpr uint32_t kOutOfRange = 0x80000000u;
 constexpr int kMaxExperts = 1024;
 constexpr size_t kLdsBytes = 160 * 1024;        // of a compute unit
 constexpr int kXcds = 8;
@@ -182,9 +194,10 @@ __device__ __forceinline__ float act_value(float g, int kind) {
 }
 __device__ __forceinline__ void act_both(float g, int kind, float& value, float& slope) {
     if (kind == kActGelu) {
-        const float s = sigmoid_f(2.0f * gelu_inner(g));
+        const float s = sigmoid_f(2.0f * gelu_inner(g)), d = s * (1.0f - s);
         value = g * s;
-        slope = s + 2.0f * g * s * (1.0f - s) * 0.7978845608028654f * (1.0f + 3 * 0.044715f * g * g);
+        // far out, where d is zero, g squared may be infinite
+        slope = d > 0.0f ? s + 2.0f * g * d * 0.7978845608028654f * (1.0f + 3 * 0.044715f * g * g) : s;
     } else {
         const float s = sigmoid_f(g);
         value = g * s;
@@ -334,7 +347,7 @@ __device__ __forceinline__ void finish(const GemmArgs& p, const Tile& t, int r_a
 }
 
 // c += b a^T in the accumulation registers.  Written out, since the compiler
-// moves 256 of those about at every turn of the loop.  s_nop 1: the states a
+// moves half of those about at every turn of the loop otherwise.  s_nop 1: the states a
 // vector instruction's result needs before the matrix core reads it.
 __device__ __forceinline__ void mfma(f32x4& c, const bf16x8& b, const bf16x8& a) {
     asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(b), "v"(a));
@@ -441,9 +454,9 @@ __device__ __forceinline__ void pipelined_tile(const GemmArgs& p, const Tile& t,
     finish<S, MF, NF>(p, t, r_at, c_at, lane, acc);
 }
 
-// The same without the register pipeline, for tiles few rows high: those are
-// bound by the weights' bytes, and several workgroups of a compute unit hide
-// each other's waits.
+// The same without the register pipeline, for the lower tiles: those are bound
+// by the weights' bytes or by latency, and several workgroups of a compute unit
+// hide each other's waits.
 template <class S>
 __device__ __forceinline__ void plain_tile(const GemmArgs& p, const Tile& t, typename S::A& la, typename S::B& lb, int K,
                                            int r_at, int c_at, int wave, int lane, lds_char* lds) {
@@ -573,42 +586,28 @@ __device__ __forceinline__ void run_product(const GemmArgs& p, int block, int G,
         typename S::A la;
         typename S::B lb;
         const uint32_t a_ldb = (uint32_t)p.a_ld * 2, b_ldb = (uint32_t)p.b_ld * 2;
+        // Rows past the region and columns past the matrix are out of the
+        // buffers' range: zeros that cost no bytes, and that are not stored.
+        auto chunk = [](int c, int n) { return c < (n >> 3) ? (uint32_t)c * 16u : kOutOfRange; };
         if constexpr (OP == kWeightGrad) {
-            // columns past the matrix repeat its last chunk; they are not stored
-            const int a_last = (p.M >> 3) - 1, b_last = (p.N >> 3) - 1;
-            la.init((const char*)p.a + t.region * a_ldb, a_ldb, wave, lane, [&](int c) {
-                const int g = (t.m0 >> 3) + c;
-                return (uint32_t)(g < a_last ? g : a_last) * 16u;
-            });
-            lb.init((const char*)p.b + t.region * b_ldb, b_ldb, wave, lane, [&](int c) {
-                const int g = (t.n0 >> 3) + c;
-                return (uint32_t)(g < b_last ? g : b_last) * 16u;
-            });
+            la.init((const char*)p.a + t.region * a_ldb, a_ldb, wave, lane, [&](int c) { return chunk((t.m0 >> 3) + c, p.M); });
+            lb.init((const char*)p.b + t.region * b_ldb, b_ldb, wave, lane, [&](int c) { return chunk((t.n0 >> 3) + c, p.N); });
         } else {
-            // rows past the region repeat its last row; they are not stored
-            const int last = t.cnt - 1 - t.m0;
+            const int left = t.cnt - t.m0;
             la.init((const char*)p.a + (t.region + t.m0) * a_ldb, a_ldb, wave, lane,
-                    [&](int r) { return (uint32_t)(r < last ? r : last) * a_ldb; });
+                    [&](int r) { return r < left ? (uint32_t)r * a_ldb : kOutOfRange; });
             const char* b = (const char*)p.b + (int64_t)t.e * p.b_expert * 2;
             if constexpr (OP == kUp) {
                 lb.init(b, b_ldb, wave, lane, [&](int r) {
                     constexpr int P = S::kPair;
                     const int j = r % P, up = j >= P / 2;
-                    int c = t.n0 + r / P * (P / 2) + j % (P / 2);
-                    c = c < p.N ? c : p.N - 1;
-                    return (uint32_t)(up ? p.N + c : c) * b_ldb;
+                    const int c = t.n0 + r / P * (P / 2) + j % (P / 2);
+                    return c < p.N ? (uint32_t)(up ? p.N + c : c) * b_ldb : kOutOfRange;
                 });
             } else if constexpr (!BS) {
-                lb.init(b, b_ldb, wave, lane, [&](int r) {
-                    const int c = t.n0 + r;
-                    return (uint32_t)(c < p.N ? c : p.N - 1) * b_ldb;
-                });
+                lb.init(b, b_ldb, wave, lane, [&](int r) { return t.n0 + r < p.N ? (uint32_t)(t.n0 + r) * b_ldb : kOutOfRange; });
             } else {
-                const int b_last = (p.N >> 3) - 1;
-                lb.init(b, b_ldb, wave, lane, [&](int c) {
-                    const int g = (t.n0 >> 3) + c;
-                    return (uint32_t)(g < b_last ? g : b_last) * 16u;
-                });
+                lb.init(b, b_ldb, wave, lane, [&](int c) { return chunk((t.n0 >> 3) + c, p.N); });
             }
         }
 
@@ -617,8 +616,12 @@ __device__ __forceinline__ void run_product(const GemmArgs& p, int block, int G,
         __builtin_amdgcn_s_barrier();
         constexpr int kAcross = BN / WN;
         if constexpr (S::kPipelined) {
-            // a tile whose lower half has no rows is shared out by columns alone
-            if (OP != kWeightGrad && BM == 2 * WM && t.cnt - t.m0 <= WM)
+            static_assert(BM == 2 * WM, "two rows of waves");
+            // a tile whose lower half or three quarters have no rows is shared
+            // out by columns alone
+            if (OP != kWeightGrad && t.cnt - t.m0 <= WM / 2)
+                pipelined_tile<S, WM / 32, WN / 32>(p, t, la, lb, K, 0, wave * (WN / 2), wave, lane, lds);
+            else if (OP != kWeightGrad && t.cnt - t.m0 <= WM)
                 pipelined_tile<S, WM / 16, WN / 32>(p, t, la, lb, K, 0, wave * (WN / 2), wave, lane, lds);
             else
                 pipelined_tile<S, WM / 16, WN / 16>(p, t, la, lb, K, wave / kAcross * WM, wave % kAcross * WN, wave, lane, lds);
@@ -637,7 +640,8 @@ __global__ void __launch_bounds__(S::kThreads) ffn_gemm_kernel(GemmArgs p) {
 
 // The three products that follow the activation's gradient, for problems of
 // less than a round of tiles each: nothing is gained by their order then, and
-// two launches are saved.
+// two launches are saved (forward and backward of 8 experts of 256 x 512, 256
+// rows: 32 us, 52 with six launches of the larger shapes).
 struct AfterArgs {
     GemmArgs rows, gate_up, down;
     int32_t grid_rows, grid_gate_up;        // workgroups of the first two
@@ -687,9 +691,19 @@ hipError_t launch(const GemmArgs& p, hipStream_t stream) {
 }
 
 // The tiles' shapes.  The widest, 256 x 256 with 8 waves and the register
-// pipeline, moves the fewest bytes through L2, which bounds these products;
-// it needs two rounds of tiles, or the last one leaves too many compute units
-// idle.
+// pipeline, moves the fewest bytes through L2, which bounds these products (of
+// the shapes below, 32 experts of 2048 rows: gate and up 3.39 ms against 4.54
+// with 128 x 128; with 4 waves it loads at two thirds of the rate).  It needs two
+// rounds of tiles, or the last one leaves too many compute units idle: 1.3
+// rounds of it took 77 and 133 us in two products where 128 x 128 took 67 and
+// 106; of the weights' gradients, whose tiles are short, 3.4 rounds took 120
+// against 112.
+// Low, 64 x 128 with three tiles in LDS, is for rows that wait for the weights:
+// 256 tokens over 64 experts of 7168 x 2048 take 992 us; 1054 with two tiles,
+// 1007 at 64 x 256, 1079 at 32 x 128.  Small is Low for less than a round of
+// tiles (8 experts of 256 x 512, 32 rows: 5.5-7.0 us a product against 6.6-11.2).
+// Few, 16 high with four tiles: one token over 8 experts 121 us; 123-130 with 64
+// columns, 126 with six tiles, 142 at 16 x 256.
 template <int OP> using Wide = Shape<OP, 256, 256, 128, 64, 64, 2, true>;
 template <int OP> using Middle = Shape<OP, 128, 128, 64, 64, 64, 2>;
 template <int OP> using Low = Shape<OP, 64, 128, 64, 32, 64, 3>;

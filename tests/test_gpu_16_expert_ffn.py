@@ -146,6 +146,29 @@ def test_out_may_be_the_pool():
     h.close()
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_pre_activations_far_out(act):
+    """Gates of huge magnitude: the activation is 0 or the gate itself, its slope 0 or 1, and nothing is NaN."""
+    import combine_ep_layout_amd as ep
+    h = ep.EpHandle(4, 1, 1, 4)
+    e = h.layout(torch.zeros(4, 1, dtype=torch.int32, device=dev()), torch.ones(4, 1, device=dev()))
+    bf = torch.bfloat16
+    gates = torch.tensor([1e30, -1e30, 3e4, -3e4], device=dev())
+    pool = torch.zeros(h.capacity_rows, 8, dtype=bf, device=dev())
+    pool[:4, 0], pool[:4, 1] = gates.to(bf), 1.0
+    wgu = torch.zeros(1, 16, 8, dtype=bf, device=dev())
+    wgu[0, :8, 0], wgu[0, 8:, 1] = 1.0, 1.0                     # gate = the first channel, up = 1
+    wd = torch.eye(8, dtype=bf, device=dev())[None].contiguous()
+    out, saved = h.expert_ffn(e, pool, wgu, wd, act, save=True)
+    want = torch.where(gates > 0, gates, torch.zeros_like(gates)).to(bf)
+    assert torch.equal(out[:4], want[:, None].expand(4, 8))
+    d = torch.empty(h.capacity_rows, 16, dtype=bf, device=dev())
+    h.expert_ffn_backward(e, torch.ones_like(pool), pool, wgu, wd, saved, act, grad_gate_up=d)
+    assert torch.equal(d[:4, :8], (gates > 0).to(bf)[:, None].expand(4, 8))
+    assert torch.equal(d[:4, 8:], want[:, None].expand(4, 8))
+    h.close()
+
+
 def test_gradient_against_differences():
     """sum(out * grad) along random directions: central differences of the float64 forward formula."""
     s = setup(60, 2, 3, 16, 64, 40, "uniform")
