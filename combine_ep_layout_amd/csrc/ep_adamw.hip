@@ -311,7 +311,8 @@ extern "C" ep_status ep_adamw(const ep_adamw_tensor* tensors, int32_t count, con
     if (!cfg || count < 0 || (count > 0 && !tensors)) return EP_ERR_INVALID_ARGUMENT;
     if (cfg->flags & ~(EP_ADAMW_PARAM_BF16 | EP_ADAMW_GRAD_BF16 | EP_ADAMW_STATE_8BIT)) return EP_ERR_INVALID_ARGUMENT;
     if (!(cfg->beta1 >= 0 && cfg->beta1 < 1 && cfg->beta2 >= 0 && cfg->beta2 < 1 && cfg->eps >= 0 &&
-          std::isfinite(cfg->eps) && std::isfinite(cfg->lr) && std::isfinite(cfg->weight_decay)) ||
+          std::isfinite(cfg->eps) && std::isfinite(cfg->lr) && std::isfinite(cfg->weight_decay) &&
+          std::isfinite(cfg->grad_scale)) ||
         (!cfg->step_dev && cfg->step < 1) || !aligned(cfg->step_dev, 8) || !aligned(cfg->grad_scale_dev, 4))
         return EP_ERR_INVALID_ARGUMENT;
     const bool eight = cfg->flags & EP_ADAMW_STATE_8BIT, pb = cfg->flags & EP_ADAMW_PARAM_BF16;

@@ -466,9 +466,9 @@ ep_status ep_expert_ffn_backward(const ep_handle* h, uint32_t epoch, const void*
  *                  rounded (with fp32 parameters only, else EP_ERR_UNSUPPORTED).
  *     n            0..2^34 (more is EP_ERR_UNSUPPORTED).  Buffers are 16-byte
  *                  aligned, scales 4-byte.
- *   cfg       host.  step >= 1, or step_dev (device int64, read when the step
- *             runs: a replayed graph takes the value it then holds; 8-byte
- *             aligned) instead; grad_scale_dev (device fp32 or NULL) is a further
+ *   cfg       host.  step >= 1, or step_dev (device int64, 8-byte aligned, read
+ *             when the step runs and at least 1 then: a replayed graph takes the
+ *             value it holds at that time) instead; grad_scale is finite; grad_scale_dev (device fp32 or NULL) is a further
  *             factor of the gradients, read when the step runs.  0 <= beta < 1,
  *             eps >= 0.
  * A buffer that is written must not share memory with any other, the same

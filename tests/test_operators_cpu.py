@@ -88,7 +88,7 @@ def test_adamw_refusals(ep):
     for bad in (dict(exp_avg_scale=0), dict(exp_avg_sq_scale=0), dict(exp_avg_scale=A[4] + 2), dict(exp_avg_scale=A[5])):
         assert adamw(ep, [{**eight, **bad}], ep.EP_ADAMW_STATE_8BIT) == INV, bad
     for bad in (dict(step=0), dict(beta1=1.0), dict(beta1=-0.1), dict(beta2=float("nan")), dict(eps=-1.0),
-                dict(eps=float("inf")), dict(lr=float("inf")), dict(weight_decay=float("nan")), dict(flags=1),
+                dict(eps=float("inf")), dict(lr=float("inf")), dict(grad_scale=float("nan")), dict(weight_decay=float("nan")), dict(flags=1),
                 dict(step_dev=A[6] + 4), dict(grad_scale_dev=A[6] + 2), dict(step_dev=A[0] + 8)):
         assert adamw(ep, [ok], **bad) == INV, bad
 
