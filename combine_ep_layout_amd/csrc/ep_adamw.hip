@@ -233,9 +233,11 @@ __global__ void __launch_bounds__(kThreads) adamw_8bit_kernel(AdamwArgs a) {
         }
         mw = encode4(mv, ms);
         vw = encode4(rv, vs);
+        // under an infinite scale code 0 reads as NaN, as the block is to read; the least code would be infinity
+        const bool finite = vs < __builtin_inff();
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-            if (rv[q] > 0.0f && ((vw >> (8 * q)) & 0xFFu) == 0) vw |= 1u << (8 * q);
+            if (finite && rv[q] > 0.0f && ((vw >> (8 * q)) & 0xFFu) == 0) vw |= 1u << (8 * q);
         if (left > 0 && (threadIdx.x & 31) == 0) {
             t.m_scale[block] = ms;
             t.v_scale[block] = vs;

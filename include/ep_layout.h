@@ -459,7 +459,9 @@ ep_status ep_expert_ffn_backward(const ep_handle* h, uint32_t epoch, const void*
  *                  least 448*2^-126; NaN takes no part) the scale is
  *                  a * (1/448) and the codes are x * ((1/a) * 448) to nearest
  *                  even, each step in fp32; a root above zero never gets code 0.
- *                  An infinity makes its block of 128 NaN, as one scale holds it.
+ *                  An infinity (in v also of a finite g whose square leaves
+ *                  fp32, from about 1.8e19 on) makes its block of 128 NaN, as
+ *                  one scale holds it.
  *     exp_avg_scale, exp_avg_sq_scale   device fp32 [ceil(n / 128)] with
  *                  EP_ADAMW_STATE_8BIT, else NULL.
  *     copy         device bf16 [n] or NULL: receives the updated fp32 parameter
