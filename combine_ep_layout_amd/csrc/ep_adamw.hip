@@ -53,12 +53,12 @@ struct Tensor {
 };
 
 struct AdamwArgs {
-    float beta1, rest1, beta2, rest2, decay, lr, eps;
+    float beta1, rest1, beta2, rest2, decay, eps;
     float step_size, root_bc2;              // lr / (1 - b1^t), sqrt(1 - b2^t)
     float grad_scale;
     const float* grad_scale_dev;
     const int64_t* step_dev;                // non-null: t is read on the device
-    double beta1_d, beta2_d;
+    double lr_d, beta1_d, beta2_d;          // what the device's step is made of, as the host's is
     int32_t count;
     int32_t first[kTensors];                // first chunk of each tensor
     Tensor t[kTensors];
@@ -103,7 +103,7 @@ __device__ __forceinline__ Scalars scalars(const AdamwArgs& a) {
     if (a.grad_scale_dev) s.grad_scale *= *a.grad_scale_dev;
     if (a.step_dev) {
         const double t = (double)*a.step_dev;
-        s.step_size = (float)((double)a.lr / (1.0 - pow(a.beta1_d, t)));
+        s.step_size = (float)(a.lr_d / (1.0 - pow(a.beta1_d, t)));
         s.root_bc2 = (float)sqrt(1.0 - pow(a.beta2_d, t));
     }
     return s;
@@ -376,8 +376,8 @@ extern "C" ep_status ep_adamw(const ep_adamw_tensor* tensors, int32_t count, con
     a.beta2 = (float)cfg->beta2;
     a.rest2 = (float)(1.0 - cfg->beta2);
     a.decay = (float)(1.0 - cfg->lr * cfg->weight_decay);
-    a.lr = (float)cfg->lr;
     a.eps = (float)cfg->eps;
+    a.lr_d = cfg->lr;
     a.beta1_d = cfg->beta1;
     a.beta2_d = cfg->beta2;
     a.grad_scale = cfg->grad_scale;

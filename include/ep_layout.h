@@ -470,9 +470,10 @@ ep_status ep_expert_ffn_backward(const ep_handle* h, uint32_t epoch, const void*
  *                  aligned, scales 4-byte.
  *   cfg       host.  step >= 1, or step_dev (device int64, 8-byte aligned, read
  *             when the step runs and at least 1 then: a replayed graph takes the
- *             value it holds at that time) instead; grad_scale is finite; grad_scale_dev (device fp32 or NULL) is a further
- *             factor of the gradients, read when the step runs.  0 <= beta < 1,
- *             eps >= 0.
+ *             value it holds at that time) instead, its factors in double from
+ *             the same numbers as the host's; grad_scale is finite; grad_scale_dev
+ *             (device fp32 or NULL) is a further factor of the gradients, read
+ *             when the step runs.  0 <= beta < 1, eps >= 0.
  * A buffer that is written must not share memory with any other, the same
  * tensor twice included (EP_ERR_INVALID_ARGUMENT).  One launch for each 52
  * tensors; capturable (the host's numbers are those of the capture). */

@@ -64,3 +64,26 @@ def test_largest_square_that_fp32_holds():
     ep.adamw(**s, step=1, **HYPER)
     root = decode(s, "exp_avg_sq")
     assert bool(root.isfinite().all()) and bool((root > 0).all())
+
+
+@pytest.mark.parametrize("eight", [False, True], ids=["fp32", "8bit"])
+@pytest.mark.parametrize("lr", [1e-3, 3e-4, 7e-4, 2.5e-3, 1e-2])
+def test_the_step_on_the_device_is_the_hosts(lr, eight):
+    """Bit for bit: an eager run and the replays of a captured one must not drift apart.  The step's two factors are
+    computed in double from the same numbers and rounded once; the two sides' pow differ by a few units in 2^-53 at most,
+    which 1 - beta2 = 1e-3 at step 1 magnifies to 2^-42, so a rounding to 2^-24 parts them once in 2^17 numbers."""
+    import combine_ep_layout_amd as ep
+    s = states(1000, seed=1)
+    if not eight:
+        g = torch.Generator(device=dev()).manual_seed(2)
+        r = lambda: torch.randn(1000, device=dev(), generator=g)
+        s.update(exp_avgs=[0.1 * r()], exp_avg_sqs=[r().square()], exp_avg_scales=None, exp_avg_sq_scales=None)
+    copy = lambda: {k: None if v is None else [t.clone() for t in v] for k, v in s.items()}
+    for beta1 in (0.9, 0.95):
+        for step in (1, 2, 3, 7, 100, 1000):
+            host, device = copy(), copy()
+            how = dict(lr=lr, beta1=beta1, beta2=0.999, eps=1e-8, weight_decay=0.1)
+            ep.adamw(**host, step=step, **how)
+            ep.adamw(**device, step=torch.tensor([step], device=dev()), **how)
+            for k, v in host.items():
+                assert v is None or torch.equal(v[0], device[k][0]), (k, beta1, step)
