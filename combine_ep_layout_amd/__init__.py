@@ -690,7 +690,8 @@ class EpHandle:
         w_down [num_experts, hidden, inter], both bf16.  With save=True returns
         (out, FfnSaved) for expert_ffn_backward; act and gate_up are the buffers
         to use for it (made when not given; act also without save, as the
-        call's workspace)."""
+        call's workspace).  out may be the pool itself without save only: the
+        backward pass reads the pool."""
         H, I = self._check_experts(pool, w_gate_up, w_down, activation)
         cap = self.capacity_rows
         if gate_up is not None and not save:

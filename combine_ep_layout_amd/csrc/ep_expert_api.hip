@@ -60,6 +60,8 @@ ep_status ep_expert_ffn(const ep_handle* h, uint32_t epoch, const void* pool, in
     if (!pool || !w_gate_up || !w_down || !act || !out || !aligned16(pool) || !aligned16(w_gate_up) ||
         !aligned16(w_down) || !aligned16(act) || !aligned16(gate_up) || !aligned16(out))
         return EP_ERR_INVALID_ARGUMENT;
+    // the backward pass that gate_up is kept for reads the pool
+    if (out == pool && gate_up) return EP_ERR_INVALID_ARGUMENT;
     const int64_t E = h->cfg.num_experts, rows_h = h->cap * hidden * 2, rows_i = h->cap * inter * 2;
     const int64_t wgu = E * inter * hidden * 4, wd = E * inter * hidden * 2, gu = rows_i * 4;
     // out may be the pool itself; nothing else written may be read or written elsewhere

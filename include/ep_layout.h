@@ -398,8 +398,9 @@ ep_status ep_dispatch_backward(const ep_handle* h, uint32_t epoch, const void* g
  *   gate_up     device fp32 [capacity_rows, 2 * inter], or NULL: receives g and
  *               u for the backward pass.
  *   out         device bf16 [capacity_rows, hidden] (ep_combine's expert_out);
- *               may be the pool itself, otherwise no buffer that is written
- *               may share memory with another (EP_ERR_INVALID_ARGUMENT).
+ *               may be the pool itself when gate_up is NULL (the backward pass
+ *               reads the pool), otherwise no buffer that is written may share
+ *               memory with another (EP_ERR_INVALID_ARGUMENT).
  * hidden % 8 == 0, inter % 8 == 0; hidden * inter above 2^29, or either above
  * 65536, is EP_ERR_UNSUPPORTED, another current device than the handle's
  * EP_ERR_INVALID_ARGUMENT.  Sums are fp32; a and out are each rounded
