@@ -189,13 +189,27 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _empty(stream, shape, dtype, device: torch.device) -> torch.Tensor:
+    """Memory that a call makes, out of the pool of the stream that the call runs on:
+    a block of the current stream's pool may still be in use by work that is queued
+    there, which the call's stream does not wait for."""
+    if stream is None or stream == torch.cuda.current_stream(device):
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _used_on(stream, *tensors) -> None:
-    """Tensors made here for a call on another stream than the current one: their
-    memory is not handed out again before that stream is past the call."""
-    if stream is not None and stream != torch.cuda.current_stream():
+    """Tensors that a call on another stream than the current one hands out or was
+    given: their memory is not handed out again before both streams are past their
+    use (a stream that the memory belongs to already is no matter)."""
+    if stream is not None:
         for t in tensors:
             if t is not None:
-                t.record_stream(stream)
+                current = torch.cuda.current_stream(t.device)
+                if stream != current:
+                    t.record_stream(stream)
+                    t.record_stream(current)
 
 
 def _check(status: int, where: str):
@@ -302,11 +316,12 @@ def cast_back(q: torch.Tensor, scales: torch.Tensor, kind: str = "ue8m0", mn_maj
     if scales.dtype != dtype or not scales.is_contiguous() or not ok:
         raise ValueError(f"scales must be {dtype} {shape}")
     if out is None:
-        out = torch.empty(rows, H, dtype=torch.bfloat16, device=q.device)
+        out = _empty(stream, (rows, H), torch.bfloat16, q.device)
     if out.dtype != torch.bfloat16 or not out.is_contiguous() or out.shape[0] < rows or out.shape[1] != H:
         raise ValueError("out must be bf16 [rows, hidden]")
     ld = scales.shape[1] if mn_major else 0
     ep_fp8_cast_back(q, scales, scale_flags(kind, mn_major), rows, ld, out, stream)
+    _used_on(stream, out)
     return out
 
 
@@ -404,8 +419,8 @@ def route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: Option
         _require(bias, torch.float32, "bias", device)
         if tuple(bias.shape) != (E,):
             raise ValueError(f"bias must be [{E}]")
-    idx = torch.empty((T, top_k), dtype=torch.int32, device=device)
-    w = torch.empty((T, top_k), dtype=torch.float32, device=device)
+    idx = _empty(stream, (T, top_k), torch.int32, device)
+    w = _empty(stream, (T, top_k), torch.float32, device)
     _check(_lib.ep_route(logits.data_ptr(), _row_stride(logits), T, E, top_k, flags,
                          None if bias is None else bias.data_ptr(), scale, idx.data_ptr(), w.data_ptr(),
                          _stream(stream)), "ep_route")
@@ -429,7 +444,7 @@ def route_backward(logits: torch.Tensor, topk_idx: torch.Tensor, grad_weights: t
     if topk_idx.dim() != 2 or topk_idx.shape[0] != T or grad_weights.shape != topk_idx.shape:
         raise ValueError("topk_idx / grad_weights must both be [num_tokens, top_k]")
     if grad_logits is None:
-        grad_logits = torch.empty((T, E), dtype=logits.dtype, device=device)
+        grad_logits = _empty(stream, (T, E), logits.dtype, device)
     elif grad_logits.dtype != logits.dtype or grad_logits.device != device or grad_logits.shape != logits.shape or \
             not _plain_rows(grad_logits):
         raise ValueError("grad_logits must be like logits")
@@ -635,12 +650,13 @@ class EpHandle:
                 or expert_out.shape[1] != H:
             raise ValueError("grad_y must be [num_tokens, H], expert_out [capacity_rows, H]")
         if grad_expert_out is None:
-            grad_expert_out = torch.empty(self.capacity_rows, H, dtype=torch.bfloat16, device=self.device)
+            grad_expert_out = _empty(stream, (self.capacity_rows, H), torch.bfloat16, self.device)
         _require(grad_expert_out, torch.bfloat16, "grad_expert_out", self.device)
         if grad_expert_out.shape[0] < self.capacity_rows or grad_expert_out.shape[1] != H:
             raise ValueError("grad_expert_out must be at least [capacity_rows, H]")
-        grad_w = torch.empty(self.num_tokens, self.top_k, dtype=torch.float32, device=self.device)
+        grad_w = _empty(stream, (self.num_tokens, self.top_k), torch.float32, self.device)
         ep_combine_backward(self._h, epoch, grad_y, expert_out, grad_expert_out, grad_w, stream)
+        _used_on(stream, grad_expert_out, grad_w)
         return grad_expert_out, grad_w
 
     def dispatch_backward(self, epoch: int, grad_pool: torch.Tensor,
@@ -650,11 +666,12 @@ class EpHandle:
         if grad_pool.shape[0] < self.capacity_rows:
             raise ValueError("grad_pool must have at least capacity_rows rows")
         if grad_x is None:
-            grad_x = torch.empty(self.num_tokens, H, dtype=torch.bfloat16, device=self.device)
+            grad_x = _empty(stream, (self.num_tokens, H), torch.bfloat16, self.device)
         _require(grad_x, torch.bfloat16, "grad_x", self.device)
         if grad_x.shape != (self.num_tokens, H):
             raise ValueError("grad_x must be [num_tokens, H]")
         ep_dispatch_backward(self._h, epoch, grad_pool, grad_x, stream)
+        _used_on(stream, grad_x)
         return grad_x
 
     def _check_rows(self, t: torch.Tensor, width: int, dtype, name: str) -> None:
@@ -696,18 +713,19 @@ class EpHandle:
         cap = self.capacity_rows
         if gate_up is not None and not save:
             raise ValueError("gate_up is written with save=True only")
+        workspace = act is None and not save
         if out is None:
-            out = torch.empty(cap, H, dtype=torch.bfloat16, device=self.device)
+            out = _empty(stream, (cap, H), torch.bfloat16, self.device)
         if act is None:
-            act = torch.empty(cap, I, dtype=torch.bfloat16, device=self.device)
+            act = _empty(stream, (cap, I), torch.bfloat16, self.device)
         if save and gate_up is None:
-            gate_up = torch.empty(cap, 2 * I, dtype=torch.float32, device=self.device)
+            gate_up = _empty(stream, (cap, 2 * I), torch.float32, self.device)
         self._check_rows(out, H, torch.bfloat16, "out")
         self._check_rows(act, I, torch.bfloat16, "act")
         if save:
             self._check_rows(gate_up, 2 * I, torch.float32, "gate_up")
         ep_expert_ffn(self._h, epoch, pool, w_gate_up, w_down, ACTIVATIONS[activation], act, gate_up, out, stream)
-        _used_on(stream, out, act, gate_up)
+        _used_on(stream, out, None if workspace else act, gate_up)
         return (out, FfnSaved(act, gate_up)) if save else out
 
     def expert_ffn_backward(self, epoch: int, grad_out: torch.Tensor, pool: torch.Tensor,
@@ -733,14 +751,15 @@ class EpHandle:
             raise TypeError(f"weight gradients must be bfloat16 or float32, got {dtype}")
         if accumulate and (len(given) < 2 or dtype != torch.float32):
             raise ValueError("accumulate needs both weight gradients, in float32")
+        workspace = grad_gate_up is None
         if grad_pool is None:
-            grad_pool = torch.empty(self.capacity_rows, H, dtype=torch.bfloat16, device=self.device)
+            grad_pool = _empty(stream, (self.capacity_rows, H), torch.bfloat16, self.device)
         if grad_w_gate_up is None:
-            grad_w_gate_up = torch.empty(E, 2 * I, H, dtype=dtype, device=self.device)
+            grad_w_gate_up = _empty(stream, (E, 2 * I, H), dtype, self.device)
         if grad_w_down is None:
-            grad_w_down = torch.empty(E, H, I, dtype=dtype, device=self.device)
+            grad_w_down = _empty(stream, (E, H, I), dtype, self.device)
         if grad_gate_up is None:
-            grad_gate_up = torch.empty(self.capacity_rows, 2 * I, dtype=torch.bfloat16, device=self.device)
+            grad_gate_up = _empty(stream, (self.capacity_rows, 2 * I), torch.bfloat16, self.device)
         self._check_rows(grad_pool, H, torch.bfloat16, "grad_pool")
         self._check_rows(grad_gate_up, 2 * I, torch.bfloat16, "grad_gate_up")
         for g, shape, name in ((grad_w_gate_up, (E, 2 * I, H), "grad_w_gate_up"),
@@ -752,7 +771,7 @@ class EpHandle:
         ep_expert_ffn_backward(self._h, epoch, grad_out, pool, w_gate_up, w_down, ACTIVATIONS[activation],
                                saved.act, saved.gate_up, flags, grad_gate_up, grad_pool, grad_w_gate_up,
                                grad_w_down, stream)
-        _used_on(stream, grad_pool, grad_gate_up, grad_w_gate_up, grad_w_down)
+        _used_on(stream, grad_pool, None if workspace else grad_gate_up, grad_w_gate_up, grad_w_down)
         return grad_pool, grad_w_gate_up, grad_w_down
 
     def borrow(self, x: torch.Tensor, stream=None) -> int:
@@ -773,11 +792,12 @@ class EpHandle:
         if expert_out.shape[0] < self.capacity_rows:
             raise ValueError(f"expert_out must have at least {self.capacity_rows} rows")
         if y is None:
-            y = torch.empty(max(self.num_tokens, 0), H, dtype=torch.bfloat16, device=self.device)
+            y = _empty(stream, (max(self.num_tokens, 0), H), torch.bfloat16, self.device)
         _require(y, torch.bfloat16, "y", self.device)
         if y.shape != (self.num_tokens, H):
             raise ValueError("y must be [num_tokens of the layout, hidden]")
         ep_combine(self._h, epoch, expert_out, y, stream)
+        _used_on(stream, y)
         return y
 
     def combine_gated(self, epoch: int, expert_out: torch.Tensor, round: int = 1,
@@ -790,11 +810,12 @@ class EpHandle:
         if expert_out.shape[0] < self.capacity_rows:
             raise ValueError(f"expert_out must have at least {self.capacity_rows} rows")
         if y is None:
-            y = torch.empty(max(self.num_tokens, 0), H, dtype=torch.bfloat16, device=self.device)
+            y = _empty(stream, (max(self.num_tokens, 0), H), torch.bfloat16, self.device)
         _require(y, torch.bfloat16, "y", self.device)
         if y.shape != (self.num_tokens, H):
             raise ValueError("y must be [num_tokens of the layout, hidden]")
         ep_combine_gated(self._h, epoch, expert_out, y, round, spin_limit_us, stream)
+        _used_on(stream, y)
         return y
 
     def tile_consume(self, seq: int, pool: torch.Tensor, pool_scales: Optional[torch.Tensor],
@@ -824,8 +845,9 @@ class EpHandle:
         """Device copy of one metadata array (see ARRAYS)."""
         which, dtype = ARRAYS[name]
         nbytes = int(_lib.ep_array_bytes(self._h, which))
-        out = torch.empty(nbytes // dtype.itemsize, dtype=dtype, device=self.device)
+        out = _empty(stream, (nbytes // dtype.itemsize,), dtype, self.device)
         _check(_lib.ep_copy_array(self._h, which, _ptr(out), nbytes, _stream(stream)), "ep_copy_array")
+        _used_on(stream, out)
         return out
 
     def counts_to_host(self, stream=None) -> Tuple[np.ndarray, int]:
