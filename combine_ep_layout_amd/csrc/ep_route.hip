@@ -405,6 +405,40 @@ constexpr uint32_t kRouteFlags = EP_ROUTE_BF16 | EP_ROUTE_SIGMOID | EP_ROUTE_NOR
 
 bool aligned(const void* p, int n) { return ((uintptr_t)p & (uintptr_t)(n - 1)) == 0; }
 
+// n rows of `width` bytes, `ld` bytes apart.
+struct Rows {
+    uintptr_t at;
+    __int128 ld, width, n;
+    Rows(const void* p, int64_t ld_, int64_t width_, int64_t n_, int size)
+        : at((uintptr_t)p), ld((__int128)ld_ * size), width((__int128)width_ * size), n(n_) {
+        if (n == 1 || ld == width) {            // one piece
+            width *= n;
+            ld = width;
+            n = 1;
+        }
+    }
+    __int128 row(__int128 i) const { return (__int128)at + i * ld; }
+    // whether a row shares a byte with [p, q)
+    bool meets(__int128 p, __int128 q) const {
+        const __int128 i = p < row(0) + width ? 0 : (p - row(0) - width) / ld + 1;      // the first row that ends behind p
+        return i < n && row(i) < q;
+    }
+    bool meets_row(const Rows& o, __int128 i) const { return meets(o.row(i), o.row(i) + o.width); }
+};
+
+// Whether two arrays share a byte: column slices of one buffer lie between each
+// other's rows and share none.
+bool share(const Rows& a, const Rows& b) {
+    if (a.row(a.n - 1) + a.width <= b.at || b.row(b.n - 1) + b.width <= a.at) return false;
+    // equal strides: where rows i and j meet, rows i - m and j - m do, and with m the smaller one is row 0
+    if (a.ld == b.ld) return a.meets_row(b, 0) || b.meets_row(a, 0);
+    const Rows& few = a.n < b.n ? a : b;
+    const Rows& many = a.n < b.n ? b : a;
+    for (__int128 i = 0; i < few.n; ++i)
+        if (many.meets_row(few, i)) return true;
+    return false;
+}
+
 // Checks that both calls share; fills what both need.
 ep_status check_route(const void* logits, int64_t ld, int32_t T, int32_t E, int32_t K, uint32_t flags,
                       float scale, RouteArgs& a) {
@@ -441,6 +475,11 @@ ep_status ep_route(const void* logits, int64_t logits_ld, int32_t num_tokens, in
     if (!topk_idx || !topk_weights || !epk::aligned(topk_idx, 4) || !epk::aligned(topk_weights, 4) ||
         !epk::aligned(bias, 4))
         return EP_ERR_INVALID_ARGUMENT;
+    const epk::Rows in(logits, logits_ld, num_experts, num_tokens, a.bf16 ? 2 : 4), idx(topk_idx, top_k, top_k, num_tokens, 4),
+        weights(topk_weights, top_k, top_k, num_tokens, 4), biases(bias, num_experts, num_experts, 1, 4);
+    if (epk::share(idx, in) || epk::share(weights, in) || epk::share(idx, weights) ||
+        (bias && (epk::share(idx, biases) || epk::share(weights, biases))))
+        return EP_ERR_INVALID_ARGUMENT;
     a.bias = bias;
     a.idx = topk_idx;
     a.weights = topk_weights;
@@ -457,6 +496,11 @@ ep_status ep_route_backward(const void* logits, int64_t logits_ld, int32_t num_t
     if (num_tokens == 0) return EP_OK;
     if (!topk_idx || !grad_weights || !grad_logits || !epk::aligned(topk_idx, 4) ||
         !epk::aligned(grad_weights, 4) || !epk::aligned(grad_logits, a.bf16 ? 2 : 4))
+        return EP_ERR_INVALID_ARGUMENT;
+    const epk::Rows out(grad_logits, grad_ld, num_experts, num_tokens, a.bf16 ? 2 : 4);
+    if (epk::share(out, epk::Rows(logits, logits_ld, num_experts, num_tokens, a.bf16 ? 2 : 4)) ||
+        epk::share(out, epk::Rows(topk_idx, top_k, top_k, num_tokens, 4)) ||
+        epk::share(out, epk::Rows(grad_weights, top_k, top_k, num_tokens, 4)))
         return EP_ERR_INVALID_ARGUMENT;
     a.chosen = topk_idx;
     a.grad_weights = grad_weights;

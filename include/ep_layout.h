@@ -186,6 +186,8 @@ int64_t ep_scale_ld(const ep_handle* h);
  *   scale         factor of every weight.
  *   topk_idx      device int32 [num_tokens, top_k], topk_weights device fp32
  *                 [num_tokens, top_k]: what ep_layout takes.
+ *                 They share no memory with each other or the inputs (else
+ *                 EP_ERR_INVALID_ARGUMENT).
  * The experts come in descending order of their scores, equal ones with the
  * lowest number first; biased scores are compared in double.  A logit (or a
  * bias) of -inf or NaN closes the expert to the token; slots that no open
@@ -204,7 +206,8 @@ ep_status ep_route(const void* logits, int64_t logits_ld, int32_t num_tokens, in
  * outside [0, num_experts) and closed experts count as masked).
  *   grad_logits   device, the logits' type, [num_tokens, num_experts], rows
  *                 grad_ld >= num_experts values apart; fully written, must not
- *                 share memory with the inputs. */
+ *                 share memory with the inputs (EP_ERR_INVALID_ARGUMENT; rows
+ *                 may lie between the logits' rows). */
 ep_status ep_route_backward(const void* logits, int64_t logits_ld, int32_t num_tokens, int32_t num_experts,
                             int32_t top_k, uint32_t flags, float scale, const int32_t* topk_idx,
                             const float* grad_weights, void* grad_logits, int64_t grad_ld, hipStream_t stream);
