@@ -34,6 +34,7 @@
 #include <utility>
 
 #include "ep_ffn.h"
+#include "ep_ffn_shape.h"
 
 namespace epk {
 namespace {
@@ -53,9 +54,6 @@ constexpr int kMaxExperts = 1024;
 constexpr size_t kLdsBytes = 160 * 1024;        // of a compute unit
 constexpr int kXcds = 8;
 constexpr int kGroupM = 8;                  // row tiles that share their column tiles' loads
-
-// The products.
-enum Op { kUp, kDown, kActGrad, kRowGrad, kWeightGrad };
 
 constexpr bool a_strided(int op) { return op == kWeightGrad; }
 constexpr bool b_strided(int op) { return op == kActGrad || op == kRowGrad || op == kWeightGrad; }
@@ -354,10 +352,6 @@ __device__ __forceinline__ void mfma(f32x4& c, const bf16x8& b, const bf16x8& a)
 }
 // The states that the matrix core's results need before another instruction
 // reads them (18 at most), for a row of fragments.
-__device__ __forceinline__ void settle(f32x4 (&c)[8]) {
-    asm volatile("s_nop 15\n\ts_nop 3"
-                 : "+a"(c[0]), "+a"(c[1]), "+a"(c[2]), "+a"(c[3]), "+a"(c[4]), "+a"(c[5]), "+a"(c[6]), "+a"(c[7]));
-}
 __device__ __forceinline__ void settle(f32x4 (&c)[2]) {
     asm volatile("s_nop 15\n\ts_nop 3" : "+a"(c[0]), "+a"(c[1]));
 }
@@ -661,21 +655,11 @@ hipError_t allow_lds(K* kernel, size_t lds) {
     return hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
 }
 
-// Row tiles of height bm that the rows of the layout can need at most.
-int64_t row_tile_bound(const GemmArgs& p, int bm) {
-    const int64_t used = p.slots < p.E ? p.slots : p.E;
-    return used + p.slots / bm;
-}
-
-template <class S>
-int64_t tile_count(const GemmArgs& p) {
-    const int64_t tiles_m = S::OP == kWeightGrad ? (int64_t)p.E * ((p.M + S::BM - 1) / S::BM) : row_tile_bound(p, S::BM);
-    return tiles_m * ((p.N + S::kCols - 1) / S::kCols);
-}
+FfnSizes sizes(const GemmArgs& p) { return {p.E, p.slots, p.M, p.N, p.num_cu}; }
 
 template <class S>
 int grid_of(const GemmArgs& p) {
-    const int64_t tiles = tile_count<S>(p), most = (int64_t)p.num_cu * (int64_t)(kLdsBytes / S::lds(p.E));
+    const int64_t tiles = ffn_tile_count((FfnOp)S::OP, {S::BM, S::BN}, sizes(p)), most = (int64_t)p.num_cu * (int64_t)(kLdsBytes / S::lds(p.E));
     return (int)(tiles < most ? tiles : most);
 }
 
@@ -690,43 +674,28 @@ hipError_t launch(const GemmArgs& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// The tiles' shapes.  The widest, 256 x 256 with 8 waves and the register
-// pipeline, moves the fewest bytes through L2, which bounds these products (of
-// the shapes below, 32 experts of 2048 rows: gate and up 3.39 ms against 4.54
-// with 128 x 128; with 4 waves it loads at two thirds of the rate).  It needs two
-// rounds of tiles, or the last one leaves too many compute units idle: 1.3
-// rounds of it took 77 and 133 us in two products where 128 x 128 took 67 and
-// 106; of the weights' gradients, whose tiles are short, 3.4 rounds took 120
-// against 112.
-// Low, 64 x 128 with three tiles in LDS, is for rows that wait for the weights:
-// 256 tokens over 64 experts of 7168 x 2048 take 992 us; 1054 with two tiles,
-// 1007 at 64 x 256, 1079 at 32 x 128.  Small is Low for less than a round of
-// tiles (8 experts of 256 x 512, 32 rows: 5.5-7.0 us a product against 6.6-11.2).
-// Few, 16 high with four tiles: one token over 8 experts 121 us; 123-130 with 64
-// columns, 126 with six tiles, 142 at 16 x 256.
-template <int OP> using Wide = Shape<OP, 256, 256, 128, 64, 64, 2, true>;
-template <int OP> using Middle = Shape<OP, 128, 128, 64, 64, 64, 2>;
-template <int OP> using Low = Shape<OP, 64, 128, 64, 32, 64, 3>;
-template <int OP> using Small = Shape<OP, 64, 64, 32, 32, 64, 4>;
-template <int OP> using Few = Shape<OP, 16, 128, 16, 32, 64, 4>;
-
-template <int OP>
-bool is_small(const GemmArgs& p) {
-    return p.slots <= (int64_t)48 * p.E && p.slots > (int64_t)16 * p.E && tile_count<Low<OP>>(p) < p.num_cu;
-}
+// The tiles' shapes (ep_ffn_shape.h, with the rule that chooses).
+template <int OP, FfnShape KIND, int WM, int WN, int ST, bool PIPELINED = false>
+using Tiles = Shape<OP, kFfnTiles[KIND].m, kFfnTiles[KIND].n, WM, WN, 64, ST, PIPELINED>;
+template <int OP> using Wide = Tiles<OP, kWide, 128, 64, 2, true>;
+template <int OP> using Middle = Tiles<OP, kMiddle, 64, 64, 2>;
+template <int OP> using Low = Tiles<OP, kLow, 64, 32, 3>;
+template <int OP> using Small = Tiles<OP, kSmall, 32, 32, 4>;
+template <int OP> using Few = Tiles<OP, kFew, 16, 32, 4>;
 
 template <int OP>
 hipError_t launch_rows(const GemmArgs& p, hipStream_t stream) {
-    const int64_t mean = (p.slots + p.E - 1) / p.E;
-    if (mean > 128 && tile_count<Wide<OP>>(p) >= 2 * p.num_cu) return launch<Wide<OP>>(p, stream);
-    if (mean > 48) return launch<Middle<OP>>(p, stream);
-    if (is_small<OP>(p)) return launch<Small<OP>>(p, stream);
-    if (mean > 16) return launch<Low<OP>>(p, stream);
-    return launch<Few<OP>>(p, stream);
+    switch (ffn_rows_shape((FfnOp)OP, sizes(p))) {
+        case kWide: return launch<Wide<OP>>(p, stream);
+        case kMiddle: return launch<Middle<OP>>(p, stream);
+        case kSmall: return launch<Small<OP>>(p, stream);
+        case kLow: return launch<Low<OP>>(p, stream);
+        default: return launch<Few<OP>>(p, stream);
+    }
 }
 
 hipError_t launch_weight_grad(const GemmArgs& p, hipStream_t stream) {
-    if (tile_count<Wide<kWeightGrad>>(p) >= 4 * p.num_cu) return launch<Wide<kWeightGrad>>(p, stream);
+    if (ffn_weight_grad_shape(sizes(p)) == kWide) return launch<Wide<kWeightGrad>>(p, stream);
     return launch<Middle<kWeightGrad>>(p, stream);
 }
 
@@ -821,8 +790,7 @@ hipError_t launch_ffn_backward(const FfnArgs& f, hipStream_t stream) {
     down.N = f.I;
     gate_up.out_f32 = down.out_f32 = f.grad_f32;
     gate_up.accumulate = down.accumulate = f.accumulate;
-    if (rows.c && gate_up.c && down.c && is_small<kRowGrad>(rows) &&
-        tile_count<Middle<kWeightGrad>>(gate_up) <= p.num_cu && tile_count<Middle<kWeightGrad>>(down) <= p.num_cu)
+    if (rows.c && gate_up.c && down.c && ffn_after_in_one(sizes(rows), sizes(gate_up), sizes(down)))
         return launch_after(rows, gate_up, down, stream);
     if (rows.c && (e = launch_rows<kRowGrad>(rows, stream)) != hipSuccess) return e;
     if (gate_up.c && (e = launch_weight_grad(gate_up, stream)) != hipSuccess) return e;
