@@ -376,7 +376,9 @@ __device__ __forceinline__ void pipelined_tile(const GemmArgs& p, const Tile& t,
     constexpr bool AS = a_strided(S::OP), BS = b_strided(S::OP);
     constexpr int LA = S::A::kLoads, L = S::kLoads;
     const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
-    const int nk = (K + S::BK - 1) / S::BK;
+    // an empty sum takes one turn, over zeros: a way around the loop would have
+    // the compiler copy the products behind it, before they have settled
+    const int nk = K > 0 ? (K + S::BK - 1) / S::BK : 1;
     f32x4 acc[MF][NF];
 #pragma unroll
     for (int i = 0; i < MF; ++i)
@@ -434,7 +436,7 @@ __device__ __forceinline__ void pipelined_tile(const GemmArgs& p, const Tile& t,
         }
     };
 #pragma unroll 1
-    for (int kt = 0; kt < nk; ++kt) {
+    for (int kt = 0;;) {
         const int slot = kt & 1;
         half(std::false_type{}, f0, f1, slot, 1, 0, 0);
         // this tile's second half has come to registers, and the next tile to
@@ -442,6 +444,7 @@ __device__ __forceinline__ void pipelined_tile(const GemmArgs& p, const Tile& t,
         wait_loads<0>();
         __builtin_amdgcn_s_barrier();
         half(std::true_type{}, f1, f0, slot ^ 1, 0, lds0 + slot * S::kStageBytes, K - (kt + 2) * S::BK);
+        if (++kt >= nk) break;
     }
 #pragma unroll
     for (int i = 0; i < MF; ++i) settle(acc[i]);
