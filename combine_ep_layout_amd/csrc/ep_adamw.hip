@@ -32,7 +32,7 @@ constexpr int kThreads = 256;
 constexpr int kBlock = 128;                 // values of one 8-bit scale
 // Values of a workgroup (a multiple of kBlock): two of a thread's vectors, so
 // that all of a workgroup's loads are in flight before its first store.  On
-// 166 M values with bf16 gradients and copies: 836 us with 2048, 858 with 4096,
+// 169.9 M values with bf16 gradients and copies: 836 us with 2048, 858 with 4096,
 // 885 with 8192, 947 with 32768 (8-bit states 466, 498, 513, 556); with cached
 // instead of non-temporal accesses 919 (533) at 8192.
 constexpr int kChunk = 2048;
@@ -286,7 +286,8 @@ struct Range {
 
 // Merges the ranges from `from` on, one kind of buffer of every tensor, into
 // those before.  A kind mostly lies in memory in the list's order, and is only
-// merged then: 43 us a step of 300 short tensors, 54 with one sort of them all.
+// merged then: the checks of 300 tensors take 11.3 us on the host, 12.2 with one
+// sort of them all; out of order 15.8 and 15.2.
 void merge_in(std::vector<Range>& r, size_t from) {
     const auto mid = r.begin() + (std::ptrdiff_t)from;
     if (!std::is_sorted(mid, r.end())) std::sort(mid, r.end());

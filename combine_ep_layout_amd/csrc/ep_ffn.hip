@@ -13,22 +13,29 @@
 // with the finished tile (the activation and the product, their derivatives,
 // or a rounding).
 //
+// a, dg and du are rounded to bf16, once each: they are operands of the next
+// products, whose matrix instructions take bf16 (in fp32 the rate would be a
+// sixteenth).  With independent roundings of at most half a step, 2^-8, that
+// makes results 2.3e-3 of their norm off where one rounding alone makes 1.7e-3.
+// g and u stay fp32, since nothing multiplies them on the matrix cores.
+//
 // Operands go from memory straight into LDS (16 bytes a lane, no registers),
 // ST tiles of 32 or 64 summed indices deep.  Where the summed index is contiguous a
 // fragment is one ds_read_b128; where it is not, the tile keeps the memory's
 // order and two transposing reads (ds_read_b64_tr_b16) make the fragment, so
 // no operand is transposed in memory.  Both layouts are swizzled by permuting
-// which 16 bytes a lane fetches, since the load itself fills LDS linearly (no
-// bank conflicts are counted).
+// which 16 bytes a lane fetches, since the load itself fills LDS linearly
+// (SQ_LDS_BANK_CONFLICT counts none in any product).
 //
 // What bounds it, measured on MI355X at 32 experts of 2048 rows, 7168 x 2048:
-// a 256 x 256 tile's matrix instructions alone run at 1.95 PFLOP/s, at the 2.1
-// GHz that their power leaves, with the LDS reads at 1.64-1.76; the loads alone
-// (64 KiB for 64 summed indices) keep pace with 1.95-2.1, which is 16 TB/s out
-// of L2, 26 bytes a cycle for each compute unit.  Together, at 1.9 GHz, they
-// reach 1.04 (gradient of the activation) to 1.29 PFLOP/s (gate and up): both
-// need most of the time, and two tiles in LDS hide only part of a load's
-// latency.  Few rows are bound by the weights' bytes instead: 5.7-5.8 TB/s.
+// 1.05 (gradient of the activation) to 1.31 PFLOP/s (pool gradient).  By the
+// counters the matrix cores are busy in 48-63 % of the cycles, at 1.9-2.0 GHz,
+// and a compute unit reads 17-21 bytes a cycle out of L2.  In variants with the
+// rest left out, a 256 x 256 tile's matrix instructions run at 1.95 PFLOP/s, with
+// the LDS reads at 1.64-1.76, and the loads (64 KiB for 64 summed indices) keep
+// pace with 1.95-2.1, 26 bytes a cycle.  So both need most of the time, and two
+// tiles in LDS hide only part of a load's latency.  Few rows are bound by the
+// weights' bytes instead: 5.7-5.8 TB/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include <utility>
