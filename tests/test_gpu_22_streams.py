@@ -132,3 +132,31 @@ def test_a_workspace_in_use_is_not_taken():
     for a, b in zip(back, calls["expert_ffn_backward"](None)):
         assert torch.equal(part(a), part(b))
     h.close()
+
+
+def test_a_side_stream_inside_a_capture():
+    """Calls on a stream that was forked from the capturing one: their memory is the graph's, and replays follow the inputs."""
+    import combine_ep_layout_amd as ep
+    say("[streams] side stream in a capture")
+    h, calls, _, part = layer()
+    names = ["expert_ffn saved", "expert_ffn_backward", "combine_backward"]
+    logits = torch.randn(T, E, device=dev())
+    run = lambda st: [*ep.route(logits, K, stream=st), *(t for n in names for t in calls[n](st))]  # noqa: E731
+    run(None)
+    torch.cuda.synchronize()
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        got = run(side)
+        main.wait_stream(side)
+        after = [t.clone() for t in got]
+    for i in range(4):
+        logits.normal_(generator=torch.Generator(device=dev()).manual_seed(i))
+        g.replay()
+        torch.cuda.synchronize()
+        seen = [part(t).clone() for t in after]
+        for a, b in zip(seen, run(None)):
+            assert torch.equal(a, part(b)), i
+        torch.cuda.synchronize()
+    h.close()
