@@ -57,6 +57,8 @@ EP_ROUTE_NORMALIZE = 1 << 13
 EP_ADAMW_PARAM_BF16 = 1 << 14
 EP_ADAMW_GRAD_BF16 = 1 << 15
 EP_ADAMW_STATE_8BIT = 1 << 16
+EP_MOE_MXFP4 = 1 << 17
+EP_MXFP4_BF16 = 1 << 18
 
 # scores of the router by name: flags
 SCORES = {"softmax": 0, "sigmoid": EP_ROUTE_SIGMOID}
@@ -94,6 +96,7 @@ EXPORTS = [
     "ep_dispatch_backward", "ep_combine_gated", "ep_fp8_cast_back", "ep_scale_ld",
     "ep_layout_noalloc", "ep_set_density_hint", "ep_layout_density", "ep_layout_dispatch",
     "ep_expert_ffn", "ep_expert_ffn_backward", "ep_route", "ep_route_backward", "ep_adamw",
+    "ep_moe_tokens", "ep_mxfp4_quantize", "ep_mxfp4_cast_back",
 ]
 
 EP_DENSITY_AUTO = 0
@@ -117,6 +120,16 @@ class _AdamwConfig(ctypes.Structure):
                 ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64),
                 ("step_dev", ctypes.c_void_p), ("grad_scale_dev", ctypes.c_void_p),
                 ("grad_scale", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
+class _MoeTokensArgs(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("x_ld", ctypes.c_int64), ("num_tokens", ctypes.c_int32),
+                ("hidden", ctypes.c_int32), ("inter", ctypes.c_int32), ("num_experts", ctypes.c_int32),
+                ("top_k", ctypes.c_int32), ("activation", ctypes.c_int32), ("flags", ctypes.c_uint32),
+                ("scale", ctypes.c_float), ("logits", ctypes.c_void_p), ("logits_ld", ctypes.c_int64),
+                ("bias", ctypes.c_void_p), ("topk_idx", ctypes.c_void_p), ("topk_weights", ctypes.c_void_p),
+                ("w_gate_up", ctypes.c_void_p), ("gate_up_scales", ctypes.c_void_p), ("w_down", ctypes.c_void_p),
+                ("down_scales", ctypes.c_void_p), ("act", ctypes.c_void_p), ("y", ctypes.c_void_p)]
 
 
 # ep_adamw_tensor, one row of an array
@@ -161,6 +174,9 @@ def _load() -> ctypes.CDLL:
         "ep_route": (st, [P, I64, I32, I32, I32, U32, P, ctypes.c_float, P, P, P]),
         "ep_route_backward": (st, [P, I64, I32, I32, I32, U32, ctypes.c_float, P, P, P, I64, P]),
         "ep_adamw": (st, [P, I32, ctypes.POINTER(_AdamwConfig), P]),
+        "ep_moe_tokens": (st, [ctypes.POINTER(_MoeTokensArgs), P]),
+        "ep_mxfp4_quantize": (st, [P, I64, U32, P, P, P]),
+        "ep_mxfp4_cast_back": (st, [P, P, I64, P, P]),
         "ep_set_density_hint": (st, [P, I32]),
         "ep_layout_density": (I32, [P, P]),
     }
@@ -453,6 +469,157 @@ def route_backward(logits: torch.Tensor, topk_idx: torch.Tensor, grad_weights: t
                                   _row_stride(grad_logits), _stream(stream)), "ep_route_backward")
     _used_on(stream, grad_logits)
     return grad_logits
+
+
+class Mxfp4(NamedTuple):
+    """Values [..., n] as 4-bit codes with an exponent byte for each 32 of them."""
+    codes: torch.Tensor         # uint8 [..., n / 2]
+    scales: torch.Tensor        # uint8 [..., n / 32]
+
+
+def mxfp4_quantize(values: torch.Tensor, out: Optional[Mxfp4] = None, stream=None) -> Mxfp4:
+    """Values (float32 or bfloat16, the last dimension a multiple of 32) as e2m1 codes,
+    two a byte with the lower index in the lower half, and one exponent byte for each
+    32: the least power of two under which none is larger than 6.  Values go to the
+    nearest code, ties to the even one; a block with an infinity or a NaN reads as NaN."""
+    if values.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"values must be float32 or bfloat16, got {values.dtype}")
+    device = values.device
+    if device.type != "cuda":
+        raise ValueError(f"values must be on a GPU, got {device}")
+    if not values.is_contiguous() or values.dim() < 1 or values.shape[-1] % 32 != 0:
+        raise ValueError("values must be contiguous, their last dimension a multiple of 32")
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return mxfp4_quantize(values, out, stream)
+    lead, n = tuple(values.shape[:-1]), values.shape[-1]
+    if out is None:
+        out = Mxfp4(_empty(stream, (*lead, n // 2), torch.uint8, device), _empty(stream, (*lead, n // 32), torch.uint8, device))
+    _check_mxfp4(out, (*lead, n), "out", device)
+    _check(_lib.ep_mxfp4_quantize(_ptr(values), values.numel(), EP_MXFP4_BF16 if values.dtype == torch.bfloat16 else 0,
+                                  _ptr(out.codes), _ptr(out.scales), _stream(stream)), "ep_mxfp4_quantize")
+    _used_on(stream, *out)
+    return Mxfp4(*out)
+
+
+def mxfp4_cast_back(q: Mxfp4, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The bf16 values that codes and scales stand for (what expert_ffn takes, for
+    batches that moe_tokens is not for)."""
+    codes, scales = q
+    device = codes.device
+    if device.type != "cuda":
+        raise ValueError(f"codes must be on a GPU, got {device}")
+    if codes.dim() < 1:
+        raise ValueError("codes must have at least one dimension")
+    shape = (*codes.shape[:-1], codes.shape[-1] * 2)
+    _check_mxfp4(q, shape, "q", device)
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return mxfp4_cast_back(q, out, stream)
+    if out is None:
+        out = _empty(stream, shape, torch.bfloat16, device)
+    _require(out, torch.bfloat16, "out", device)
+    if tuple(out.shape) != shape:
+        raise ValueError(f"out must be {list(shape)}")
+    _check(_lib.ep_mxfp4_cast_back(_ptr(codes), _ptr(scales), out.numel(), _ptr(out), _stream(stream)), "ep_mxfp4_cast_back")
+    _used_on(stream, out)
+    return out
+
+
+def _check_mxfp4(q, shape, name: str, device: torch.device) -> None:
+    """Codes and scales of values of this shape."""
+    codes, scales = q
+    _require(codes, torch.uint8, f"{name}.codes", device)
+    _require(scales, torch.uint8, f"{name}.scales", device)
+    lead, n = tuple(shape[:-1]), shape[-1]
+    if n % 32 != 0 or tuple(codes.shape) != (*lead, n // 2) or tuple(scales.shape) != (*lead, n // 32):
+        raise ValueError(f"{name} must be the codes and scales of {list(shape)} values, the last a multiple of 32")
+
+
+def moe_tokens(x: torch.Tensor, w_gate_up, w_down, logits: Optional[torch.Tensor] = None, top_k: Optional[int] = None,
+               score: str = "softmax", bias: Optional[torch.Tensor] = None, normalize: bool = True, scale: float = 1.0,
+               topk_idx: Optional[torch.Tensor] = None, topk_weights: Optional[torch.Tensor] = None,
+               activation: str = "silu", y: Optional[torch.Tensor] = None, stream=None
+               ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """A whole layer for up to 64 tokens, without a handle: (y, topk_idx, topk_weights),
+    y [num_tokens, hidden] bf16.
+
+    x [num_tokens, hidden] bf16, rows may be strided.  The experts' weights are those of
+    EpHandle.expert_ffn, w_gate_up [num_experts, 2 * inter, hidden] and w_down
+    [num_experts, hidden, inter] in bf16, or both Mxfp4 of these shapes.  With logits
+    and top_k the choice is route()'s (score, bias, normalize and scale as there);
+    otherwise topk_idx int32 and topk_weights float32 [num_tokens, top_k] make it, and
+    an index outside [0, num_experts) is masked."""
+    four = isinstance(w_gate_up, tuple)
+    if four != isinstance(w_down, tuple):
+        raise TypeError("w_gate_up and w_down must both be bfloat16 tensors or both Mxfp4")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
+    if x.dtype is not torch.bfloat16:
+        raise TypeError(f"x must be {torch.bfloat16}, got {x.dtype}")
+    device = x.device
+    if device.type != "cuda":
+        raise ValueError(f"x must be on a GPU, got {device}")
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return moe_tokens(x, w_gate_up, w_down, logits, top_k, score, bias, normalize, scale, topk_idx, topk_weights,
+                              activation, y, stream)
+    if x.dim() != 2 or not _plain_rows(x):
+        raise ValueError("x must be [num_tokens, hidden] with contiguous rows that do not overlap")
+    T, H = x.shape
+    down = w_down[0] if four else w_down
+    if down.dim() != 3 or down.shape[1] != H:
+        raise ValueError(f"w_down must be [num_experts, {H}, inter]")
+    E, I = down.shape[0], down.shape[2] * (2 if four else 1)
+    for w, shape, name in ((w_gate_up, (E, 2 * I, H), "w_gate_up"), (w_down, (E, H, I), "w_down")):
+        if four:
+            _check_mxfp4(w, shape, name, device)
+        else:
+            _require(w, torch.bfloat16, name, device)
+            if tuple(w.shape) != shape:
+                raise ValueError(f"{name} must be {list(shape)}")
+    a = _MoeTokensArgs(x=x.data_ptr(), x_ld=_row_stride(x), num_tokens=T, hidden=H, inter=I, num_experts=E,
+                       activation=ACTIVATIONS[activation], scale=scale, flags=EP_MOE_MXFP4 if four else 0)
+    if logits is not None:
+        if topk_idx is not None or topk_weights is not None or top_k is None:
+            raise ValueError("give logits with top_k, or topk_idx with topk_weights")
+        a.flags |= _route_args(logits, score, normalize)
+        if logits.device != device or tuple(logits.shape) != (T, E):
+            raise ValueError(f"logits must be [{T}, {E}] on {device}")
+        a.logits, a.logits_ld = logits.data_ptr(), _row_stride(logits)
+        if bias is not None:
+            _require(bias, torch.float32, "bias", device)
+            if tuple(bias.shape) != (E,):
+                raise ValueError(f"bias must be [{E}]")
+            a.bias = bias.data_ptr()
+        topk_idx = _empty(stream, (T, top_k), torch.int32, device)
+        topk_weights = _empty(stream, (T, top_k), torch.float32, device)
+    elif topk_idx is None or topk_weights is None or bias is not None:
+        raise ValueError("give logits with top_k, or topk_idx with topk_weights and no bias")
+    else:
+        _require(topk_idx, torch.int32, "topk_idx", device)
+        _require(topk_weights, torch.float32, "topk_weights", device)
+        if topk_idx.dim() != 2 or topk_idx.shape[0] != T or topk_weights.shape != topk_idx.shape or \
+                top_k not in (None, topk_idx.shape[1]):
+            raise ValueError("topk_idx / topk_weights must both be [num_tokens, top_k]")
+    a.top_k = K = topk_idx.shape[1]
+    a.topk_idx, a.topk_weights = topk_idx.data_ptr(), topk_weights.data_ptr()
+    if four:
+        a.w_gate_up, a.gate_up_scales = w_gate_up[0].data_ptr(), w_gate_up[1].data_ptr()
+        a.w_down, a.down_scales = w_down[0].data_ptr(), w_down[1].data_ptr()
+    else:
+        a.w_gate_up, a.w_down = w_gate_up.data_ptr(), w_down.data_ptr()
+    act = _empty(stream, (T * K, I), torch.bfloat16, device)
+    if y is None:
+        y = _empty(stream, (T, H), torch.bfloat16, device)
+    else:
+        _require(y, torch.bfloat16, "y", device)
+        if tuple(y.shape) != (T, H):
+            raise ValueError(f"y must be [{T}, {H}]")
+    a.act, a.y = act.data_ptr(), y.data_ptr()
+    _check(_lib.ep_moe_tokens(ctypes.byref(a), _stream(stream)), "ep_moe_tokens")
+    _used_on(stream, y, topk_idx, topk_weights)
+    return y, topk_idx, topk_weights
 
 
 _GATHER_ERRORS = {1: (ValueError, "must have as many tensors as params"), 2: (TypeError, "must hold dense tensors"),

@@ -5,12 +5,9 @@
 #include <stdint.h>
 #include <hip/hip_runtime.h>
 
-namespace epk {
+#include "ep_act.h"
 
-enum ActKind : int32_t {
-    kActSilu = 0,
-    kActGelu = 1,               // tanh form
-};
+namespace epk {
 
 // One grouped product (see ep_ffn.hip).
 struct GemmArgs {

@@ -51,7 +51,7 @@
  *     as their 16-bit patterns.
  *   - HIP graph capture: ep_layout, ep_dispatch, ep_combine, ep_combine_gated,
  *     the backward calls, ep_fp8_cast_back, ep_route, ep_expert_ffn, their
- *     backward calls and ep_adamw only launch kernels (nothing is
+ *     backward calls, ep_adamw, ep_moe_tokens and the ep_mxfp4 calls only launch kernels (nothing is
  *     allocated and no memory is set through the runtime), so they can be
  *     captured and replayed.  The host-side counters advance when a call is
  *     captured, not when it is replayed: a replay repeats the captured epoch,
@@ -443,6 +443,83 @@ ep_status ep_expert_ffn_backward(const ep_handle* h, uint32_t epoch, const void*
                                  int32_t activation, const void* act, const float* gate_up, uint32_t flags,
                                  void* grad_gate_up, void* grad_pool, void* grad_w_gate_up,
                                  void* grad_w_down, hipStream_t stream);
+
+/* A whole layer for a few tokens, from the router's logits (or a choice that is
+ * made already) to y, without a handle, a layout or a pool:
+ *     y_t = sum_k w_tk Wd[e] a,  a = act(Wg[e] x_t) * (Wu[e] x_t),  e = e_tk.
+ * The buffers are on the current device.
+ *   x               device bf16 [num_tokens, hidden], rows x_ld >= hidden values
+ *                   apart (a multiple of 8, at most 2^23).
+ *   num_tokens      0..64 (more is EP_ERR_UNSUPPORTED: lay out and dispatch).
+ *   hidden, inter   multiples of 8, with EP_MOE_MXFP4 of 32; limits as in
+ *                   ep_expert_ffn.  activation: EP_ACT_*.
+ *   num_experts     1..1024; top_k 1..32.
+ *   logits          device [num_tokens, num_experts], rows logits_ld apart: the
+ *                   choice is ep_route's, with EP_ROUTE_* in flags, bias and
+ *                   scale, and topk_idx, topk_weights receive it.
+ *                   NULL: topk_idx and topk_weights are inputs; EP_ROUTE_* and
+ *                   bias are refused, scale is not used.
+ *   topk_idx        device int32, topk_weights device fp32 [num_tokens, top_k].
+ *                   As an input an index outside [0, num_experts) is masked, and
+ *                   an expert that a token names twice counts with both weights.
+ *   w_gate_up       device bf16 [num_experts, 2 * inter, hidden], w_down device
+ *                   bf16 [num_experts, hidden, inter], as in ep_expert_ffn; with
+ *                   EP_MOE_MXFP4 the codes of ep_mxfp4_quantize, and
+ *                   gate_up_scales [num_experts, 2 * inter, hidden / 32],
+ *                   down_scales [num_experts, hidden, inter / 32] their bytes.
+ *   act             device bf16 [num_tokens * top_k, inter]: workspace.
+ *   y               device bf16 [num_tokens, hidden]; a token without an expert
+ *                   gets zeros.
+ * Pointers are 16-byte aligned; logits, bias, topk_idx and topk_weights as
+ * ep_route wants them, scale bytes anyhow.  Nothing that is written shares
+ * memory with anything else (EP_ERR_INVALID_ARGUMENT).  Sums are fp32 in a fixed
+ * order, weights included; a and y are each rounded once.  A token's row of y
+ * depends on nothing of the other tokens but the order of its sums: infinities
+ * and NaN stay in their rows.  Two launches, three with logits of more than
+ * 8 tokens or 256 experts; capturable. */
+#define EP_MOE_MXFP4 (1u << 17)
+typedef struct ep_moe_tokens_args {
+    const void* x;
+    int64_t x_ld;
+    int32_t num_tokens;
+    int32_t hidden;
+    int32_t inter;
+    int32_t num_experts;
+    int32_t top_k;
+    int32_t activation;
+    uint32_t flags;
+    float scale;
+    const void* logits;
+    int64_t logits_ld;
+    const float* bias;
+    int32_t* topk_idx;
+    float* topk_weights;
+    const void* w_gate_up;
+    const uint8_t* gate_up_scales;
+    const void* w_down;
+    const uint8_t* down_scales;
+    void* act;
+    void* y;
+} ep_moe_tokens_args;
+ep_status ep_moe_tokens(const ep_moe_tokens_args* args, hipStream_t stream);
+
+/* Values as 4-bit codes with an exponent byte for each 32 of them, the form
+ * that ep_moe_tokens takes weights in, and back.
+ *   values  device fp32 (EP_MXFP4_BF16: bf16) [n]; n % 32 == 0, n <= 2^38.
+ *   codes   device [n / 2]: e2m1 (0, 1/2, 1, 3/2, 2, 3, 4, 6; bit 3 the sign),
+ *           two a byte, the lower index in the lower half.
+ *   scales  device [n / 32]: byte b stands for 2^(b - 127).
+ * A block's byte is the least one under which none of its values is larger than
+ * 6 (0 for a block of zeros); values go to the nearest code, ties to the even
+ * one.  A block with an infinity or a NaN gets byte 255, which reads as NaN.
+ * The cast back writes bf16; code times 2^(b - 127) is exact there but for
+ * the subnormals and for 2^128 and more, which is infinity.
+ * values, codes and out are 16-byte aligned; what is written shares no memory
+ * with anything else (EP_ERR_INVALID_ARGUMENT).  One launch; capturable. */
+#define EP_MXFP4_BF16 (1u << 18)
+ep_status ep_mxfp4_quantize(const void* values, int64_t n, uint32_t flags, void* codes, uint8_t* scales,
+                            hipStream_t stream);
+ep_status ep_mxfp4_cast_back(const void* codes, const uint8_t* scales, int64_t n, void* out, hipStream_t stream);
 
 /* One AdamW step over many tensors (decoupled weight decay), the experts'
  * weights with the gradients of ep_expert_ffn_backward among them.  Per value,
