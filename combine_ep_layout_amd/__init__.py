@@ -59,6 +59,9 @@ EP_ADAMW_GRAD_BF16 = 1 << 15
 EP_ADAMW_STATE_8BIT = 1 << 16
 EP_MOE_MXFP4 = 1 << 17
 EP_MXFP4_BF16 = 1 << 18
+EP_MUON_PARAM_BF16 = 1 << 19
+EP_MUON_GRAD_BF16 = 1 << 20
+EP_MUON_NESTEROV = 1 << 21
 
 # scores of the router by name: flags
 SCORES = {"softmax": 0, "sigmoid": EP_ROUTE_SIGMOID}
@@ -97,6 +100,7 @@ EXPORTS = [
     "ep_layout_noalloc", "ep_set_density_hint", "ep_layout_density", "ep_layout_dispatch",
     "ep_expert_ffn", "ep_expert_ffn_backward", "ep_route", "ep_route_backward", "ep_adamw",
     "ep_moe_tokens", "ep_mxfp4_quantize", "ep_mxfp4_cast_back",
+    "ep_muon_workspace_bytes", "ep_muon", "ep_orthogonalize",
 ]
 
 EP_DENSITY_AUTO = 0
@@ -131,6 +135,15 @@ class _MoeTokensArgs(ctypes.Structure):
                 ("w_gate_up", ctypes.c_void_p), ("gate_up_scales", ctypes.c_void_p), ("w_down", ctypes.c_void_p),
                 ("down_scales", ctypes.c_void_p), ("act", ctypes.c_void_p), ("y", ctypes.c_void_p)]
 
+
+class _MuonConfig(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_double) for k in ("lr", "momentum", "weight_decay", "scale", "eps", "a", "b", "c")] + \
+               [("steps", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+# ep_muon_tensor, one row of an array
+_MUON_TENSOR = np.dtype([(k, np.uint64) for k in ("param", "grad", "momentum", "copy")] +
+                        [("batch", np.int64), ("rows", np.int32), ("cols", np.int32)])
 
 # ep_adamw_tensor, one row of an array
 _ADAMW_TENSOR = np.dtype([(k, np.uint64) for k in ("param", "grad", "exp_avg", "exp_avg_sq", "exp_avg_scale",
@@ -177,6 +190,10 @@ def _load() -> ctypes.CDLL:
         "ep_moe_tokens": (st, [ctypes.POINTER(_MoeTokensArgs), P]),
         "ep_mxfp4_quantize": (st, [P, I64, U32, P, P, P]),
         "ep_mxfp4_cast_back": (st, [P, P, I64, P, P]),
+        "ep_muon_workspace_bytes": (I64, [P, I32]),
+        "ep_muon": (st, [P, I32, ctypes.POINTER(_MuonConfig), P, I64, P]),
+        "ep_orthogonalize": (st, [P, I64, I32, I32, I32, ctypes.POINTER(ctypes.c_double), ctypes.c_double, U32, P, I64,
+                                  P, P]),
         "ep_set_density_hint": (st, [P, I32]),
         "ep_layout_density": (I32, [P, P]),
     }
@@ -700,6 +717,108 @@ def adamw(params, grads, exp_avgs, exp_avg_sqs, step, lr: float = 1e-3, beta1: f
         cfg.grad_scale = float(grad_scale)
     with torch.cuda.device(device):
         _check(_lib.ep_adamw(t.ctypes.data_as(ctypes.c_void_p), n, ctypes.byref(cfg), _stream(stream)), "ep_adamw")
+
+
+NEWTON_SCHULZ = (3.4445, -4.775, 2.0315)
+
+
+def _muon_workspace(table: np.ndarray, workspace: Optional[torch.Tensor], stream, device: torch.device) -> torch.Tensor:
+    """The given workspace, or one of the size that is of use."""
+    if workspace is not None:
+        _require(workspace, torch.uint8, "workspace", device)
+        return workspace
+    need = int(_lib.ep_muon_workspace_bytes(table.ctypes.data_as(ctypes.c_void_p), len(table)))
+    if need < 0:
+        raise EpError(EP_ERR_UNSUPPORTED, "ep_muon_workspace_bytes")
+    return _empty(stream, (need,), torch.uint8, device)
+
+
+def orthogonalize(x: torch.Tensor, steps: int = 5, coefficients=NEWTON_SCHULZ, eps: float = 1e-7,
+                  out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
+    """x [..., rows, cols] (float32 or bfloat16) orthogonalised, matrix by matrix, in bf16:
+    `steps` times X = a X + (b G + c G G) X with G = X X^T (on the shorter side) and
+    coefficients (a, b, c), from X = x / (|x| + eps).
+
+    workspace: a uint8 tensor to use (made when not given; with less than it would
+    be, fewer matrices go through at once)."""
+    if x.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"x must be float32 or bfloat16, got {x.dtype}")
+    device = x.device
+    if device.type != "cuda":
+        raise ValueError(f"x must be on a GPU, got {device}")
+    if x.dim() < 2 or not x.is_contiguous():
+        raise ValueError("x must be contiguous [..., rows, cols]")
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return orthogonalize(x, steps, coefficients, eps, out, workspace, stream)
+    rows, cols = x.shape[-2:]
+    batch = x.numel() // (rows * cols) if rows and cols else 0
+    if out is None:
+        out = _empty(stream, tuple(x.shape), torch.bfloat16, device)
+    _require(out, torch.bfloat16, "out", device)
+    if out.shape != x.shape:
+        raise ValueError(f"out must be {list(x.shape)}")
+    table = np.zeros(1, _MUON_TENSOR)
+    table["batch"], table["rows"], table["cols"] = batch, rows, cols
+    workspace = _muon_workspace(table, workspace, stream, device)
+    abc = (ctypes.c_double * 3)(*coefficients)
+    _check(_lib.ep_orthogonalize(_ptr(x), batch, rows, cols, steps, abc, eps,
+                                 EP_MUON_GRAD_BF16 if x.dtype == torch.bfloat16 else 0, _ptr(workspace),
+                                 workspace.numel(), _ptr(out), _stream(stream)), "ep_orthogonalize")
+    _used_on(stream, out)
+    return out
+
+
+def muon(params, grads, momenta, lr: float = 1e-3, momentum: float = 0.95, weight_decay: float = 1e-2,
+         nesterov: bool = True, steps: int = 5, coefficients=NEWTON_SCHULZ, eps: float = 1e-7,
+         scale: Optional[float] = None, copies=None, workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """One step over lists of tensors of matrices [..., rows, cols], in place, whose update
+    is orthogonalised matrix by matrix (orthogonalize): the momentum is
+    momentum * m + (1 - momentum) * g, the update X of it (nesterov: of its mix with g),
+    and p = p (1 - lr weight_decay) - lr scale X.
+
+    params float32 or bfloat16, grads float32 or bfloat16 (each list of one type),
+    momenta float32; copies: bfloat16 tensors that receive the updated float32
+    parameters.  scale None: 0.2 sqrt(max(rows, cols)), which makes the update as
+    large as adamw's.  The experts' gate and up matrices count as two when
+    w_gate_up is given as w_gate_up.view(2 * num_experts, inter, hidden).
+    workspace: a uint8 tensor to use, as for orthogonalize."""
+    n = len(params)
+    if n == 0:
+        return
+    device = params[0].device
+    if device.type != "cuda":
+        raise ValueError(f"params must be on a GPU, got {device}")
+    p_dtype, g_dtype = params[0].dtype, grads[0].dtype if len(grads) else None
+    for dtype, name in ((p_dtype, "params"), (g_dtype, "grads")):
+        if dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"{name} must be float32 or bfloat16, got {dtype}")
+    if scale is not None and not scale > 0:
+        raise ValueError("scale must be above zero")
+    lists = [("param", params, p_dtype), ("grad", grads, g_dtype), ("momentum", momenta, torch.float32)]
+    if copies is not None:
+        lists.append(("copy", copies, torch.bfloat16))
+    t = np.zeros(n, [*_MUON_TENSOR.descr, ("n", np.int64)])
+    for i, (key, tensors, dtype) in enumerate(lists):
+        _gather(t, key, tensors, dtype, device, per=1 if i else 0)
+    for i, p in enumerate(params):
+        if p.dim() < 2 or any(other[i].shape != p.shape for _, other, _ in lists[1:]):
+            raise ValueError(f"tensor {i}: params, grads, momenta and copies must have one shape [..., rows, cols]")
+        rows, cols = p.shape[-2:]
+        t[i]["rows"], t[i]["cols"] = rows, cols
+        t[i]["batch"] = p.numel() // (rows * cols) if rows and cols else 0
+    table = np.empty(n, _MUON_TENSOR)
+    for key in _MUON_TENSOR.names:
+        table[key] = t[key]
+    cfg = _MuonConfig(lr=lr, momentum=momentum, weight_decay=weight_decay, scale=scale or 0.0, eps=eps, a=coefficients[0],
+                      b=coefficients[1], c=coefficients[2], steps=steps)
+    cfg.flags = (EP_MUON_PARAM_BF16 if p_dtype == torch.bfloat16 else 0) | \
+        (EP_MUON_GRAD_BF16 if g_dtype == torch.bfloat16 else 0) | (EP_MUON_NESTEROV if nesterov else 0)
+    with torch.cuda.device(device):
+        workspace = _muon_workspace(table, workspace, stream, device)
+        _check(_lib.ep_muon(table.ctypes.data_as(ctypes.c_void_p), n, ctypes.byref(cfg), _ptr(workspace), workspace.numel(),
+                            _stream(stream)), "ep_muon")
 
 
 # ------------------------------------------------------------- convenience --

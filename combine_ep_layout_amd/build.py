@@ -20,7 +20,8 @@ LIB = os.path.join(PKG, "libep_layout.so")
 SOURCES = [os.path.join(CSRC, "ep_kernels.hip"), os.path.join(CSRC, "ep_expert_api.hip"),
            os.path.join(CSRC, "ep_noalloc.hip"), os.path.join(CSRC, "ep_ffn.hip"),
            os.path.join(CSRC, "ep_route.hip"), os.path.join(CSRC, "ep_adamw.hip"),
-           os.path.join(CSRC, "ep_tokens.hip"), os.path.join(CSRC, "ep_mxfp4.hip")]
+           os.path.join(CSRC, "ep_tokens.hip"), os.path.join(CSRC, "ep_mxfp4.hip"),
+           os.path.join(CSRC, "ep_muon.hip")]
 CEILING_LIB = os.path.join(PKG, "libep_ceiling.so")
 CEILING_SOURCES = [os.path.join(CSRC, "ep_ceiling.hip")]
 TORCH_LIB = os.path.join(PKG, "_ep_torch.so")

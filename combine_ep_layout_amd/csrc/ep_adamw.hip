@@ -18,11 +18,11 @@
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
-#include <algorithm>
 #include <new>
 #include <vector>
 
 #include "ep_layout.h"
+#include "ep_ranges.h"
 
 namespace epk {
 namespace {
@@ -261,8 +261,6 @@ __global__ void __launch_bounds__(kThreads) adamw_8bit_kernel(AdamwArgs a) {
     }
 }
 
-bool aligned(const void* p, int n) { return ((uintptr_t)p & (uintptr_t)(n - 1)) == 0; }
-
 void launch(const AdamwArgs& a, uint32_t flags, int grid, hipStream_t stream) {
     const bool pb = flags & EP_ADAMW_PARAM_BF16, gb = flags & EP_ADAMW_GRAD_BF16;
     if (flags & EP_ADAMW_STATE_8BIT) {
@@ -276,33 +274,6 @@ void launch(const AdamwArgs& a, uint32_t flags, int grid, hipStream_t stream) {
         else if (gb) adamw_kernel<false, true><<<grid, kThreads, 0, stream>>>(a);
         else adamw_kernel<false, false><<<grid, kThreads, 0, stream>>>(a);
     }
-}
-
-struct Range {
-    uintptr_t at, end;
-    bool wrote;
-    bool operator<(const Range& o) const { return at < o.at; }
-};
-
-// Merges the ranges from `from` on, one kind of buffer of every tensor, into
-// those before.  A kind mostly lies in memory in the list's order, and is only
-// merged then: the checks of 300 tensors take 11.3 us on the host, 12.2 with one
-// sort of them all; out of order 15.8 and 15.2.
-void merge_in(std::vector<Range>& r, size_t from) {
-    const auto mid = r.begin() + (std::ptrdiff_t)from;
-    if (!std::is_sorted(mid, r.end())) std::sort(mid, r.end());
-    std::inplace_merge(r.begin(), mid, r.end());
-}
-
-// Whether a buffer that is written shares memory with another buffer (r in order).
-bool shared(const std::vector<Range>& r) {
-    uintptr_t any = 0, written = 0;         // furthest end so far, of all and of those written
-    for (const Range& x : r) {
-        if (x.at < written || (x.wrote && x.at < any)) return true;
-        any = std::max(any, x.end);
-        if (x.wrote) written = std::max(written, x.end);
-    }
-    return false;
 }
 
 }  // namespace

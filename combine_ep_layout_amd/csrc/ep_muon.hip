@@ -1,0 +1,699 @@
+// gfx950 kernels that orthogonalise matrices by Newton-Schulz products, and of
+// the optimiser step on it, with their C entry points.
+//
+// A matrix U, laid as m x n with m <= n (a tall one transposed), becomes
+//     X = U / (|U| + eps),  then `steps` times  X = a X + P X,
+//     G = X X^T,  P = b G + c G G,
+// which takes every singular value through a s + b s^3 + c s^5 and leaves the
+// singular vectors: with the usual coefficients those above 1/500 of the norm
+// end between 0.7 and 1.2.  G and P are symmetric, so only the tiles on and below
+// the diagonal are computed: m^2 n + m^3 + 2 m^2 n operations a step.
+//
+// The products run on the matrix cores in fp16 with fp32 sums.  fp16 and not
+// bf16: everything here is bounded (|X| <= 1.2 in the 2-norm), so powers of two
+// put the values into fp16's range for good, and its 11 bits leave results 1.6e-3
+// off in the norm where bf16 makes 1.1e-2.  X itself is kept as two fp16 values,
+// hi and 2^-11 lo: the first steps multiply small singular values by a = 3.4 each, and
+// with them whatever rounding X had; the products see hi alone, where a rounding
+// is no more than its share of P X (matrices of rank 16 in noise-free form:
+// 4e-4 instead of 4.5e-2).
+//
+// One launch serves all matrices of a list: their shapes and addresses travel
+// in the kernel's arguments.  Step by step: the norms (with the momentum), the
+// split into hi and lo, then three products each; the last one writes the
+// results, or updates the parameters, from its registers.
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+#include <new>
+#include <vector>
+
+#include "ep_gemm.h"
+#include "ep_layout.h"
+#include "ep_ranges.h"
+
+namespace epk {
+namespace {
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+// The products: G, P, the next X, and the last X into the results (of tall
+// matrices with the sums of a lane along the other side).
+enum Op { kGram, kPoly, kNext, kLast, kLastTall };
+constexpr bool is_update(int op) { return op >= kNext; }
+
+constexpr int kProblems = 40;               // shapes of a launch: the arguments stay below 4 KiB
+constexpr int kMaxSide = 1 << 16;
+constexpr int64_t kMaxMatrix = 1 << 29;     // values: a matrix of fp16 stays below 2 GiB
+constexpr int kGroupM = 8;                  // row tiles that share their column tiles' loads
+// Powers of two that G and P are held at: G's least entries, 1 / (m sqrt(n)) of
+// the first step, are normal numbers, and |P| <= |b| + |c| is far from 65504.
+constexpr float kGramScale = 1024.0f;
+constexpr float kLow = 2048.0f;             // lo is held at this many times its value
+constexpr int kPartials = 256;              // sums of squares of a matrix at most
+constexpr int kThreads = 256;
+constexpr int kSplit = 64;                  // side of a tile of the split
+constexpr int kSplitTiles = 8;              // tiles of a workgroup
+
+// `batch` matrices of one shape.  The workspace holds, each for all of them:
+// hi (two, by turns), lo [m, ld_n], g, p [m, ld_m] in fp16, and the partial sums.
+struct Problem {
+    const void* x;              // the gradient, or what is orthogonalised
+    float* momentum;            // null: x alone
+    void* param;                // fp32 or bf16 [rows, cols]; the result (bf16) without momentum
+    __bf16* copy;               // may be null
+    char* ws;
+    int32_t m, n, ld_m, ld_n;
+    int32_t batch;
+    int32_t tall;               // x and param are [n, m]
+    int32_t partials;           // of a matrix
+    float scale;                // the power of two that X is held at
+    float step;                 // learning rate times the shape's factor
+
+    __host__ __device__ int64_t x_size() const { return (int64_t)m * ld_n; }
+    __host__ __device__ int64_t g_size() const { return (int64_t)m * ld_m; }
+    __device__ _Float16* hi(int turn) const { return (_Float16*)ws + turn * batch * x_size(); }
+    __device__ _Float16* lo() const { return (_Float16*)ws + 2 * batch * x_size(); }
+    __device__ _Float16* g() const { return (_Float16*)ws + 3 * batch * x_size(); }
+    __device__ _Float16* p() const { return (_Float16*)ws + 3 * batch * x_size() + batch * g_size(); }
+    __device__ double* sums() const { return (double*)((_Float16*)ws + 3 * batch * x_size() + 2 * batch * g_size()); }
+    // bytes of one matrix; a multiple of 16, since the leading dimensions are multiples of 8
+    __host__ int64_t ws_each() const { return 6 * x_size() + 4 * g_size() + (int64_t)partials * 8; }
+};
+
+struct GroupArgs {
+    int32_t count;
+    int32_t turn;               // which hi is read
+    int32_t x_bf16, param_bf16, nesterov;
+    float a, b, c;
+    float mu, rest_mu;          // momentum
+    float eps;
+    float decay;
+    int32_t first[kProblems + 1];           // first tile (or workgroup) of each problem
+    Problem p[kProblems];
+};
+static_assert(sizeof(GroupArgs) <= 4096, "kernel arguments");
+
+// The problem that item i belongs to.
+__device__ __forceinline__ int find_problem(const GroupArgs& a, int i) {
+    const int lane = threadIdx.x & (kWave - 1);
+    return __builtin_popcountll(__ballot(lane < a.count && a.first[lane] <= i)) - 1;
+}
+
+__device__ __forceinline__ float load_x(const GroupArgs& a, const void* x, int64_t i) {
+    return a.x_bf16 ? (float)((const __bf16*)x)[i] : ((const float*)x)[i];
+}
+
+// The update's value from the gradient and the new momentum.
+__device__ __forceinline__ float mix(const GroupArgs& a, float g, float m) {
+    return a.nesterov ? a.rest_mu * g + a.mu * m : m;
+}
+
+// The momentum, and the sums of squares of the update, in double: neither tiny
+// nor huge gradients leave its range.
+__global__ void __launch_bounds__(kThreads) muon_sums_kernel(GroupArgs a) {
+    __shared__ double part[kThreads / kWave];
+    const int i = find_problem(a, blockIdx.x), tid = threadIdx.x;
+    const Problem& p = a.p[i];
+    const int local = blockIdx.x - a.first[i], mat = local / p.partials, k = local - mat * p.partials;
+    const int64_t n = (int64_t)p.m * p.n, at = mat * n, step = (int64_t)p.partials * kThreads;
+    double sum = 0.0;
+#pragma unroll 4
+    for (int64_t j = (int64_t)k * kThreads + tid; j < n; j += step) {
+        float u = load_x(a, p.x, at + j);
+        if (p.momentum) {
+            const float m = a.mu * p.momentum[at + j] + a.rest_mu * u;
+            p.momentum[at + j] = m;
+            u = mix(a, u, m);
+        }
+        sum += (double)u * (double)u;
+    }
+#pragma unroll
+    for (int d = kWave / 2; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
+    if ((tid & (kWave - 1)) == 0) part[tid / kWave] = sum;
+    __syncthreads();
+    if (tid == 0) p.sums()[local] = (part[0] + part[1]) + (part[2] + part[3]);
+}
+
+__device__ __forceinline__ void split(float v, _Float16& hi, _Float16& lo) {
+    hi = (_Float16)v;
+    lo = (_Float16)((v - (float)hi) * kLow);
+}
+
+// X over its norm, as hi and lo, tall matrices transposed; columns past n are zeros.
+__global__ void __launch_bounds__(kThreads) muon_split_kernel(GroupArgs a) {
+    __shared__ float tile[kSplit][kSplit + 1];
+    __shared__ double part[kThreads / kWave];
+    const int i = find_problem(a, blockIdx.x), tid = threadIdx.x;
+    const Problem& p = a.p[i];
+    const int down = (p.m + kSplit - 1) / kSplit, across = (p.ld_n + kSplit * kSplitTiles - 1) / (kSplit * kSplitTiles);
+    const int local = blockIdx.x - a.first[i], mat = local / (down * across), t = local - mat * down * across;
+    double sum = 0.0;
+    for (int k = tid; k < p.partials; k += kThreads) sum += p.sums()[mat * p.partials + k];
+#pragma unroll
+    for (int d = kWave / 2; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
+    if ((tid & (kWave - 1)) == 0) part[tid / kWave] = sum;
+    __syncthreads();
+    const double norm = sqrt((part[0] + part[1]) + (part[2] + part[3]));
+    const double s = norm == 0.0 ? 0.0 : (double)p.scale / (norm + (double)a.eps);       // a matrix of zeros stays one
+    const int64_t at = (int64_t)mat * p.m * p.n;
+    _Float16* const hi = p.hi(0) + mat * p.x_size();
+    _Float16* const lo = p.lo() + mat * p.x_size();
+    const int r0 = t / across * kSplit;
+    for (int c0 = t % across * kSplitTiles * kSplit, k = 0; k < kSplitTiles && c0 < p.ld_n; ++k, c0 += kSplit) {
+        // in the order of memory: [r][c], tall [c][r]
+        for (int j = tid; j < kSplit * kSplit; j += kThreads) {
+            const int y = j / kSplit, x = j % kSplit;
+            const int r = r0 + (p.tall ? x : y), c = c0 + (p.tall ? y : x);
+            float u = 0.0f;
+            if (r < p.m && c < p.n) {
+                const int64_t from = at + (p.tall ? (int64_t)c * p.m + r : (int64_t)r * p.n + c);
+                u = load_x(a, p.x, from);
+                if (p.momentum) u = mix(a, u, p.momentum[from]);
+            }
+            tile[p.tall ? x : y][p.tall ? y : x] = (float)((double)u * s);
+        }
+        __syncthreads();
+        for (int j = tid; j < kSplit * kSplit / 8; j += kThreads) {
+            const int y = j / (kSplit / 8), x = j % (kSplit / 8) * 8;
+            if (r0 + y < p.m && c0 + x < p.ld_n) {
+                f16x8 h, l;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    _Float16 vh, vl;
+                    split(tile[y][x + q], vh, vl);
+                    h[q] = vh;
+                    l[q] = vl;
+                }
+                const int64_t to = (int64_t)(r0 + y) * p.ld_n + c0 + x;
+                *(f16x8*)(hi + to) = h;
+                *(f16x8*)(lo + to) = l;
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// BM x BN tiles, WM x WN of it to each wave, ST LDS tiles of each operand.
+template <int OP_, int BM_, int BN_, int WM_, int WN_, int ST_, bool PIPELINED>
+struct Shape {
+    static constexpr int OP = OP_, BM = BM_, BN = BN_, WM = WM_, WN = WN_, BK = 64, ST = ST_;
+    static constexpr int kWaves = (BM / WM) * (BN / WN);
+    static constexpr int kThreads = kWaves * kWave;
+    static constexpr int kStageBytes = (BM + BN) * BK * 2;
+    static constexpr bool kPipelined = PIPELINED;
+    static constexpr bool kAStrided = false, kBStrided = is_update(OP), kF16 = true, kSwap = OP == kLastTall;
+    using A = Loader<BM, BK, kAStrided, kWaves>;
+    using B = Loader<BN, BK, kBStrided, kWaves>;
+    static constexpr int kLoads = A::kLoads + B::kLoads;
+    static constexpr size_t kLds = (size_t)ST * kStageBytes;
+};
+
+// Tiles of one matrix.
+template <int BM, int BN>
+__host__ __device__ inline int64_t tiles_of(int op, int m, int ld_n) {
+    const int64_t down = (m + BM - 1) / BM;
+    return is_update(op) ? down * ((ld_n + BN - 1) / BN) : down * (down + 1) / 2;
+}
+
+// The eight sums of a lane out of two fragments, consecutive along the side that
+// its sums lie on; lane l's first is at eight_at(l) of the fragments' places.
+__device__ __forceinline__ void eight(const f32x4& v0, const f32x4& v1, float (&o)[8]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v0[q]), __float_as_uint(v1[q]), false, false);
+        o[q] = __uint_as_float(r[0]);
+        o[4 + q] = __uint_as_float(r[1]);
+    }
+}
+__device__ __forceinline__ int eight_at(int lane) { return (lane & 16) + (lane >> 5) * 8; }
+
+// Results of consecutive values: bf16, or the parameters' step and their copy.
+__device__ __forceinline__ void write_results(const GroupArgs& a, const Problem& p, int64_t at, int left, const float (&v)[8]) {
+    const float back = 1.0f / p.scale;          // a power of two
+    if (!p.momentum) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (q < left) ((__bf16*)p.param)[at + q] = (__bf16)(v[q] * back);
+        return;
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        if (q >= left) break;
+        const float old = a.param_bf16 ? (float)((const __bf16*)p.param)[at + q] : ((const float*)p.param)[at + q];
+        const float now = old * a.decay - p.step * (v[q] * back);
+        if (a.param_bf16) ((__bf16*)p.param)[at + q] = (__bf16)now;
+        else ((float*)p.param)[at + q] = now;
+        if (p.copy) p.copy[at + q] = (__bf16)now;
+    }
+}
+
+// A wave's part of a finished tile: rows from r_at, columns from c_at.
+template <class S, int MF, int NF>
+__device__ __forceinline__ void finish(const GroupArgs& a, const Problem& p, int mat, int r_at, int c_at, bool mirror, int lane,
+                                       const f32x4 (&acc)[MF][NF]) {
+    constexpr int OP = S::OP;
+    if constexpr (OP == kLastTall) {
+        // lane l holds column l % 16; its rows lie together in the result
+        const _Float16* const hi = p.hi(a.turn) + mat * p.x_size();
+        const _Float16* const lo = p.lo() + mat * p.x_size();
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+            const int c = c_at + j * 16 + (lane & 15);
+#pragma unroll
+            for (int i = 0; i < MF; i += 2) {
+                float v[8];
+                eight(acc[i][j], acc[i + 1][j], v);
+                const int r = r_at + i * 16 + eight_at(lane);
+                if (c >= p.n || r >= p.m) continue;
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    if (r + q < p.m) {
+                        const int64_t from = (int64_t)(r + q) * p.ld_n + c;
+                        v[q] = a.a * ((float)hi[from] + (float)lo[from] * (1.0f / kLow)) + v[q] * (1.0f / kGramScale);
+                    }
+                write_results(a, p, (int64_t)mat * p.m * p.n + (int64_t)c * p.m + r, p.m - r, v);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < MF; ++i) {
+            const int r = r_at + i * 16 + (lane & 15);
+#pragma unroll
+            for (int j = 0; j < NF; j += 2) {
+                float v[8];
+                eight(acc[i][j], acc[i][j + 1], v);         // every lane takes part
+                const int c = c_at + j * 16 + eight_at(lane);
+                if constexpr (OP == kGram || OP == kPoly) {
+                    const _Float16* const g = p.g() + mat * p.g_size();
+                    _Float16* const out = (OP == kGram ? p.g() : p.p()) + mat * p.g_size();
+                    if (r >= p.ld_m || c >= p.ld_m) continue;
+                    const bool real = r < p.m;
+                    f16x8 w;
+                    if constexpr (OP == kGram) {
+                        const float s = kGramScale / (p.scale * p.scale);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) w[q] = (_Float16)(v[q] * s);
+                    } else {
+                        f16x8 old = {0, 0, 0, 0, 0, 0, 0, 0};
+                        if (real) old = *(const f16x8*)(g + (int64_t)r * p.ld_m + c);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) w[q] = (_Float16)(a.b * (float)old[q] + a.c * (v[q] * (1.0f / kGramScale)));
+                    }
+                    if (real) *(f16x8*)(out + (int64_t)r * p.ld_m + c) = w;
+                    if (mirror)
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            if (c + q < p.m) out[(int64_t)(c + q) * p.ld_m + r] = w[q];
+                } else {
+                    if (r >= p.m || c >= p.ld_n) continue;
+                    const int64_t at = mat * p.x_size() + (int64_t)r * p.ld_n + c;
+                    const f16x8 h = *(const f16x8*)(p.hi(a.turn) + at), l = *(const f16x8*)(p.lo() + at);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        v[q] = a.a * ((float)h[q] + (float)l[q] * (1.0f / kLow)) + v[q] * (1.0f / kGramScale);
+                    if constexpr (OP == kNext) {
+                        f16x8 nh, nl;
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            _Float16 vh, vl;
+                            split(v[q], vh, vl);
+                            nh[q] = vh;
+                            nl[q] = vl;
+                        }
+                        *(f16x8*)(p.hi(a.turn ^ 1) + at) = nh;
+                        *(f16x8*)(p.lo() + at) = nl;
+                    } else {
+                        write_results(a, p, (int64_t)mat * p.m * p.n + (int64_t)r * p.n + c, p.n - c, v);
+                    }
+                }
+            }
+        }
+    }
+}
+
+template <class S>
+__global__ void __launch_bounds__(S::kThreads) muon_gemm_kernel(GroupArgs a) {
+    extern __shared__ __attribute__((aligned(1024))) char smem[];
+    constexpr int OP = S::OP, BM = S::BM, BN = S::BN, WM = S::WM, WN = S::WN;
+    lds_char* lds = (lds_char*)smem;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6), block = blockIdx.x, G = gridDim.x;
+    // Workgroup b runs on XCD b mod 8: consecutive tiles, which share rows and
+    // columns, go to one XCD and its L2.
+    const int first = (G % kXcds == 0) ? (block % kXcds) * (G / kXcds) + block / kXcds : block;
+    const int total = a.first[a.count];
+    for (int t = first; t < total; t += G) {
+        const int i = uni(find_problem(a, t));
+        const Problem& p = a.p[i];
+        const int per = (int)tiles_of<BM, BN>(OP, p.m, p.ld_n), local = t - a.first[i];
+        const int mat = local / per, in = local - mat * per;
+        int mt, nt;
+        if constexpr (is_update(OP)) {
+            const int tiles_m = (p.m + BM - 1) / BM, tiles_n = (p.ld_n + BN - 1) / BN;
+            const int grp = in / (kGroupM * tiles_n), rest = in - grp * kGroupM * tiles_n;
+            const int rows = tiles_m - grp * kGroupM < kGroupM ? tiles_m - grp * kGroupM : kGroupM;
+            nt = rest / rows;
+            mt = grp * kGroupM + rest - nt * rows;
+        } else {
+            // the largest mt with mt (mt + 1) / 2 <= in
+            mt = (int)((sqrtf(8.0f * (float)in + 1.0f) - 1.0f) * 0.5f);
+            while (mt * (mt + 1) / 2 > in) --mt;
+            while ((mt + 1) * (mt + 2) / 2 <= in) ++mt;
+            nt = in - mt * (mt + 1) / 2;
+        }
+        mt = uni(mt);
+        nt = uni(nt);
+        const int m0 = mt * BM, n0 = nt * BN;
+        const int K = OP == kGram ? p.ld_n : p.m;
+        const _Float16* const x = p.hi(a.turn) + mat * p.x_size();
+        const _Float16* const left = OP == kGram ? x : (OP == kPoly ? p.g() : p.p()) + mat * p.g_size();
+        const _Float16* const right = OP == kPoly ? left : x;
+        const uint32_t a_ld = (uint32_t)(OP == kGram ? p.ld_n : p.ld_m) * 2, b_ld = (uint32_t)(OP == kPoly ? p.ld_m : p.ld_n) * 2;
+        typename S::A la;
+        typename S::B lb;
+        // rows and columns past the matrix are out of the buffers' range: zeros
+        la.init(left + (int64_t)m0 * (a_ld / 2), a_ld, wave, lane, [&](int r) { return m0 + r < p.m ? (uint32_t)r * a_ld : kOutOfRange; });
+        if constexpr (is_update(OP))
+            lb.init(right, b_ld, wave, lane,
+                    [&](int c) { return n0 / 8 + c < p.ld_n / 8 ? (uint32_t)(n0 / 8 + c) * 16u : kOutOfRange; });
+        else
+            lb.init(right + (int64_t)n0 * (b_ld / 2), b_ld, wave, lane,
+                    [&](int r) { return n0 + r < p.m ? (uint32_t)r * b_ld : kOutOfRange; });
+        // the last tile's reads are done before its LDS is filled again
+        wait_loads<0>();
+        __builtin_amdgcn_s_barrier();
+        constexpr int kAcross = BN / WN;
+        const int r = wave / kAcross * WM, c = wave % kAcross * WN;
+        auto done = [&](const f32x4 (&acc)[WM / 16][WN / 16]) {
+            finish<S, WM / 16, WN / 16>(a, p, mat, m0 + r, n0 + c, mt != nt, lane, acc);
+        };
+        if constexpr (S::kPipelined) pipelined_tile<S, WM / 16, WN / 16>(la, lb, K, r, c, wave, lane, lds, done);
+        else plain_tile<S>(la, lb, K, r, c, wave, lane, lds, done);
+    }
+    wait_loads<0>();        // no load into LDS outlives the workgroup
+}
+
+// Wide tiles when they fill the compute units, lower ones when they do not.
+template <int OP> using Wide = Shape<OP, 256, 256, 128, 64, 2, true>;
+template <int OP> using Middle = Shape<OP, 128, 128, 64, 64, 2, false>;
+template <int OP> using Small = Shape<OP, 64, 64, 32, 32, 4, false>;
+
+template <class S>
+int64_t set_tiles(GroupArgs& a) {
+    int64_t total = 0;
+    for (int i = 0; i < a.count; ++i) {
+        a.first[i] = (int32_t)total;
+        total += a.p[i].batch * tiles_of<S::BM, S::BN>(S::OP, a.p[i].m, a.p[i].ld_n);
+    }
+    a.first[a.count] = (int32_t)total;
+    return total;
+}
+
+template <class S>
+hipError_t launch_shape(GroupArgs& a, int num_cu, hipStream_t stream) {
+    const int64_t tiles = set_tiles<S>(a), most = (int64_t)num_cu * (int64_t)(kLdsBytes / S::kLds);
+    hipError_t e = hipFuncSetAttribute((const void*)muon_gemm_kernel<S>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)S::kLds);
+    if (e != hipSuccess) return e;
+    muon_gemm_kernel<S><<<(int)(tiles < most ? tiles : most), S::kThreads, S::kLds, stream>>>(a);
+    return hipGetLastError();
+}
+
+template <int OP>
+hipError_t launch_product(GroupArgs& a, int num_cu, hipStream_t stream) {
+    if (set_tiles<Wide<OP>>(a) >= num_cu) return launch_shape<Wide<OP>>(a, num_cu, stream);
+    if (set_tiles<Middle<OP>>(a) >= num_cu) return launch_shape<Middle<OP>>(a, num_cu, stream);
+    return launch_shape<Small<OP>>(a, num_cu, stream);
+}
+
+// The last products of the wide or of the tall problems.
+template <int OP>
+hipError_t launch_last(const GroupArgs& a, int num_cu, hipStream_t stream) {
+    GroupArgs some = a;
+    some.count = 0;
+    for (int i = 0; i < a.count; ++i)
+        if (a.p[i].tall == (OP == kLastTall)) some.p[some.count++] = a.p[i];
+    return some.count ? launch_product<OP>(some, num_cu, stream) : hipSuccess;
+}
+
+hipError_t run_group(GroupArgs& a, int steps, int num_cu, hipStream_t stream) {
+    int64_t blocks = 0;
+    for (int i = 0; i < a.count; ++i) {
+        a.first[i] = (int32_t)blocks;
+        blocks += (int64_t)a.p[i].batch * a.p[i].partials;
+    }
+    a.turn = 0;
+    muon_sums_kernel<<<(int)blocks, kThreads, 0, stream>>>(a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    blocks = 0;
+    for (int i = 0; i < a.count; ++i) {
+        a.first[i] = (int32_t)blocks;
+        const Problem& p = a.p[i];
+        blocks += (int64_t)p.batch * ((p.m + kSplit - 1) / kSplit) * ((p.ld_n + kSplit * kSplitTiles - 1) / (kSplit * kSplitTiles));
+    }
+    muon_split_kernel<<<(int)blocks, kThreads, 0, stream>>>(a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    for (int s = 0; s < steps; ++s) {
+        if ((e = launch_product<kGram>(a, num_cu, stream)) != hipSuccess) return e;
+        if ((e = launch_product<kPoly>(a, num_cu, stream)) != hipSuccess) return e;
+        if (s + 1 < steps) e = launch_product<kNext>(a, num_cu, stream);
+        else if ((e = launch_last<kLast>(a, num_cu, stream)) == hipSuccess) e = launch_last<kLastTall>(a, num_cu, stream);
+        if (e != hipSuccess) return e;
+        a.turn ^= 1;
+    }
+    return hipSuccess;
+}
+
+int up8(int v) { return (v + 7) / 8 * 8; }
+
+// One matrix of a shape (batch 1).
+Problem problem_of(int32_t rows, int32_t cols) {
+    Problem p{};
+    p.tall = rows > cols;
+    p.m = p.tall ? cols : rows;
+    p.n = p.tall ? rows : cols;
+    p.ld_m = up8(p.m);
+    p.ld_n = up8(p.n);
+    p.batch = 1;
+    const int64_t n = (int64_t)rows * cols, chunks = (n + 8191) / 8192;
+    p.partials = (int)(chunks < kPartials ? (chunks + 1) / 2 * 2 : kPartials);      // even: 16 bytes
+    p.scale = exp2f(roundf(0.5f * log2f((float)p.n)));
+    return p;
+}
+
+ep_status check_shape(int64_t batch, int32_t rows, int32_t cols) {
+    if (batch < 0 || rows < 0 || cols < 0) return EP_ERR_INVALID_ARGUMENT;
+    if (rows > kMaxSide || cols > kMaxSide || (int64_t)rows * cols > kMaxMatrix || batch > (1 << 20)) return EP_ERR_UNSUPPORTED;
+    return EP_OK;
+}
+
+// What a call would like to have: everything at once up to 4 GiB, and room for
+// the largest matrix in any case.
+constexpr int64_t kLikedBytes = (int64_t)4 << 30;
+
+struct Shapes {
+    int64_t batch;
+    int32_t rows, cols;
+};
+
+int64_t workspace_of(const std::vector<Shapes>& shapes) {
+    int64_t all = 0, largest = 0;
+    for (const Shapes& s : shapes) {
+        if (s.batch == 0 || s.rows == 0 || s.cols == 0) continue;
+        const int64_t each = problem_of(s.rows, s.cols).ws_each();
+        largest = each > largest ? each : largest;
+        const int64_t room = kLikedBytes - all;
+        all += s.batch <= room / each ? s.batch * each : room;
+    }
+    return all > largest ? all : largest;
+}
+
+// Problems put into groups as the workspace and the launches hold them, and run.
+struct Runner {
+    GroupArgs a{};
+    char* ws;
+    int64_t bytes, used = 0;
+    int64_t tiles = 0;
+    int steps, num_cu;
+    hipStream_t stream;
+
+    hipError_t flush() {
+        hipError_t e = a.count ? run_group(a, steps, num_cu, stream) : hipSuccess;
+        a.count = 0;
+        used = tiles = 0;
+        return e;
+    }
+    // size of param and copy in bytes a value, x as the flags say
+    hipError_t add(Problem p, int64_t batch, int64_t x_size, int64_t param_size) {
+        const int64_t each = p.ws_each(), n = (int64_t)p.m * p.n;
+        // a launch's tiles stay far below 2^31
+        const int64_t tiles_each = tiles_of<64, 64>(kNext, p.m, p.ld_n) + p.partials, most_tiles = (int64_t)1 << 28;
+        for (int64_t done = 0; done < batch;) {
+            int64_t fit = (bytes - used) / each;
+            const int64_t fit_tiles = (most_tiles - tiles) / tiles_each;
+            fit = fit < fit_tiles ? fit : fit_tiles;
+            if (a.count == kProblems || fit < 1) {
+                const hipError_t e = flush();
+                if (e != hipSuccess) return e;
+                continue;
+            }
+            const int64_t k = batch - done < fit ? batch - done : fit;
+            Problem& q = a.p[a.count++] = p;
+            q.batch = (int32_t)k;
+            q.x = (const char*)p.x + done * n * x_size;
+            if (p.momentum) q.momentum = p.momentum + done * n;
+            q.param = (char*)p.param + done * n * param_size;
+            if (p.copy) q.copy = p.copy + done * n;
+            q.ws = ws + used;
+            used += k * each;
+            tiles += k * tiles_each;
+            done += k;
+        }
+        return hipSuccess;
+    }
+};
+
+bool cu_count(int& n) {
+    int device = 0;
+    return hipGetDevice(&device) == hipSuccess &&
+           hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, device) == hipSuccess && n > 0;
+}
+
+bool fine(const double (&c)[3]) { return std::isfinite(c[0]) && std::isfinite(c[1]) && std::isfinite(c[2]); }
+
+}  // namespace
+}  // namespace epk
+
+extern "C" {
+
+int64_t ep_muon_workspace_bytes(const ep_muon_tensor* tensors, int32_t count) {
+    using namespace epk;
+    if (count < 0 || (count > 0 && !tensors)) return -1;
+    try {
+        std::vector<Shapes> shapes;
+        shapes.reserve((size_t)count);
+        for (int32_t i = 0; i < count; ++i) {
+            if (check_shape(tensors[i].batch, tensors[i].rows, tensors[i].cols) != EP_OK) return -1;
+            shapes.push_back({tensors[i].batch, tensors[i].rows, tensors[i].cols});
+        }
+        return workspace_of(shapes);
+    } catch (const std::bad_alloc&) {
+        return -1;
+    }
+}
+
+ep_status ep_orthogonalize(const void* x, int64_t batch, int32_t rows, int32_t cols, int32_t steps,
+                           const double coefficients[3], double eps, uint32_t flags, void* workspace,
+                           int64_t workspace_bytes, void* out, hipStream_t stream) {
+    using namespace epk;
+    if (flags & ~EP_MUON_GRAD_BF16) return EP_ERR_INVALID_ARGUMENT;
+    const ep_status st = check_shape(batch, rows, cols);
+    if (st != EP_OK) return st;
+    if (steps < 1 || steps > 100 || !(eps >= 0) || !std::isfinite(eps)) return EP_ERR_INVALID_ARGUMENT;
+    double k[3] = {3.4445, -4.775, 2.0315};
+    if (coefficients)
+        for (int i = 0; i < 3; ++i) k[i] = coefficients[i];
+    if (!fine(k)) return EP_ERR_INVALID_ARGUMENT;
+    if (batch == 0 || rows == 0 || cols == 0) return EP_OK;
+    const bool bf16 = flags & EP_MUON_GRAD_BF16;
+    const Problem one = problem_of(rows, cols);
+    const int64_t n = batch * rows * cols, xs = bf16 ? 2 : 4;
+    if (!x || !out || !workspace || !aligned(x, 16) || !aligned(out, 16) || !aligned(workspace, 16) ||
+        workspace_bytes < one.ws_each())
+        return EP_ERR_INVALID_ARGUMENT;
+    const Rows rx(x, n, n, 1, (int)xs), ro(out, n, n, 1, 2), rw(workspace, workspace_bytes, workspace_bytes, 1, 1);
+    if (share(rx, ro) || share(rx, rw) || share(ro, rw)) return EP_ERR_INVALID_ARGUMENT;
+    Runner run;
+    run.ws = (char*)workspace;
+    run.bytes = workspace_bytes;
+    run.steps = steps;
+    run.stream = stream;
+    if (!cu_count(run.num_cu)) return EP_ERR_HIP;
+    run.a.x_bf16 = bf16;
+    run.a.a = (float)k[0];
+    run.a.b = (float)k[1];
+    run.a.c = (float)k[2];
+    run.a.eps = (float)eps;
+    Problem p = one;
+    p.x = x;
+    p.param = out;
+    if (run.add(p, batch, xs, 2) != hipSuccess || run.flush() != hipSuccess) return EP_ERR_HIP;
+    return EP_OK;
+}
+
+ep_status ep_muon(const ep_muon_tensor* tensors, int32_t count, const ep_muon_config* cfg, void* workspace,
+                  int64_t workspace_bytes, hipStream_t stream) {
+    using namespace epk;
+    if (!cfg || count < 0 || (count > 0 && !tensors)) return EP_ERR_INVALID_ARGUMENT;
+    if (cfg->flags & ~(EP_MUON_PARAM_BF16 | EP_MUON_GRAD_BF16 | EP_MUON_NESTEROV)) return EP_ERR_INVALID_ARGUMENT;
+    const double k[3] = {cfg->a, cfg->b, cfg->c};
+    if (!(cfg->momentum >= 0 && cfg->momentum < 1 && cfg->eps >= 0 && cfg->scale >= 0) || !std::isfinite(cfg->eps) ||
+        !std::isfinite(cfg->scale) || !std::isfinite(cfg->lr) || !std::isfinite(cfg->weight_decay) || !fine(k) || cfg->steps < 1 ||
+        cfg->steps > 100)
+        return EP_ERR_INVALID_ARGUMENT;
+    const bool pb = cfg->flags & EP_MUON_PARAM_BF16, gb = cfg->flags & EP_MUON_GRAD_BF16;
+    const int64_t ps = pb ? 2 : 4, gs = gb ? 2 : 4;
+    auto none = [](const ep_muon_tensor& t) { return t.batch == 0 || t.rows == 0 || t.cols == 0; };
+    bool any = false;
+    try {
+        std::vector<Range> ranges;
+        ranges.reserve((size_t)count * 4 + 1);
+        auto put = [&](const void* p, int64_t n, bool w) {
+            if (p) ranges.push_back({(uintptr_t)p, (uintptr_t)p + (uintptr_t)n, w});
+        };
+        for (int32_t i = 0; i < count; ++i) {
+            const ep_muon_tensor& t = tensors[i];
+            const ep_status st = check_shape(t.batch, t.rows, t.cols);
+            if (st != EP_OK) return st;
+            if (t.copy && pb) return EP_ERR_UNSUPPORTED;        // bf16 parameters are their own copy
+            if (none(t)) continue;
+            any = true;
+            if (!t.param || !t.grad || !t.momentum || !aligned(t.param, 16) || !aligned(t.grad, 16) ||
+                !aligned(t.momentum, 16) || !aligned(t.copy, 16) || workspace_bytes < problem_of(t.rows, t.cols).ws_each())
+                return EP_ERR_INVALID_ARGUMENT;
+            const int64_t n = t.batch * t.rows * t.cols;
+            put(t.param, n * ps, true);
+            put(t.grad, n * gs, false);
+            put(t.momentum, n * 4, true);
+            put(t.copy, n * 2, true);
+        }
+        if (!any) return EP_OK;
+        if (!workspace || !aligned(workspace, 16)) return EP_ERR_INVALID_ARGUMENT;
+        put(workspace, workspace_bytes, true);
+        std::sort(ranges.begin(), ranges.end());
+        if (shared(ranges)) return EP_ERR_INVALID_ARGUMENT;
+    } catch (const std::bad_alloc&) {
+        return EP_ERR_OUT_OF_MEMORY;
+    }
+    Runner run;
+    run.ws = (char*)workspace;
+    run.bytes = workspace_bytes;
+    run.steps = cfg->steps;
+    run.stream = stream;
+    if (!cu_count(run.num_cu)) return EP_ERR_HIP;
+    GroupArgs& a = run.a;
+    a.x_bf16 = gb;
+    a.param_bf16 = pb;
+    a.nesterov = (cfg->flags & EP_MUON_NESTEROV) != 0;
+    a.a = (float)cfg->a;
+    a.b = (float)cfg->b;
+    a.c = (float)cfg->c;
+    a.mu = (float)cfg->momentum;
+    a.rest_mu = (float)(1.0 - cfg->momentum);
+    a.eps = (float)cfg->eps;
+    a.decay = (float)(1.0 - cfg->lr * cfg->weight_decay);
+    for (int32_t i = 0; i < count; ++i) {
+        const ep_muon_tensor& t = tensors[i];
+        if (none(t)) continue;
+        Problem p = problem_of(t.rows, t.cols);
+        p.x = t.grad;
+        p.momentum = t.momentum;
+        p.param = t.param;
+        p.copy = (__bf16*)t.copy;
+        p.step = (float)(cfg->lr * (cfg->scale > 0 ? cfg->scale : 0.2 * sqrt((double)p.n)));
+        if (run.add(p, t.batch, gs, ps) != hipSuccess) return EP_ERR_HIP;
+    }
+    return run.flush() == hipSuccess ? EP_OK : EP_ERR_HIP;
+}
+
+}  // extern "C"

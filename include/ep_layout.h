@@ -51,7 +51,8 @@
  *     as their 16-bit patterns.
  *   - HIP graph capture: ep_layout, ep_dispatch, ep_combine, ep_combine_gated,
  *     the backward calls, ep_fp8_cast_back, ep_route, ep_expert_ffn, their
- *     backward calls, ep_adamw, ep_moe_tokens and the ep_mxfp4 calls only launch kernels (nothing is
+ *     backward calls, ep_adamw, ep_moe_tokens, the ep_mxfp4 calls, ep_muon and
+ *     ep_orthogonalize only launch kernels (nothing is
  *     allocated and no memory is set through the runtime), so they can be
  *     captured and replayed.  The host-side counters advance when a call is
  *     captured, not when it is replayed: a replay repeats the captured epoch,
@@ -584,6 +585,77 @@ typedef struct ep_adamw_config {
     uint32_t flags;
 } ep_adamw_config;
 ep_status ep_adamw(const ep_adamw_tensor* tensors, int32_t count, const ep_adamw_config* cfg, hipStream_t stream);
+
+/* The optimiser step on matrices whose update is orthogonalised, over many
+ * tensors at once, each a batch of rows x cols matrices (the experts' weights
+ * with the gradients of ep_expert_ffn_backward among them).  Per matrix:
+ *     m = mu m + (1 - mu) g
+ *     U = (1 - mu) g + mu m with EP_MUON_NESTEROV, else m
+ *     X = U / (|U| + eps), |.| the root of the sum of squares
+ *     steps times: X = a X + (b G + c G G) X, G = X X^T (rows <= cols; for tall
+ *         matrices X (b G + c G G), G = X^T X)
+ *     p = p (1 - lr weight_decay) - lr scale X
+ * The steps take each singular value s of X through a s + b s^3 + c s^5, five of
+ * them with the coefficients 3.4445, -4.775, 2.0315 into 0.7..1.2 or so.
+ *   tensors      host array; batch of rows x cols matrices, contiguous:
+ *     param      device fp32 (EP_MUON_PARAM_BF16: bf16), updated.
+ *     grad       device fp32 (EP_MUON_GRAD_BF16: bf16).
+ *     momentum   device fp32, updated.
+ *     copy       device bf16 or NULL: receives the updated parameters (not with
+ *                EP_MUON_PARAM_BF16: EP_ERR_UNSUPPORTED).
+ *   cfg          0 <= momentum < 1, eps >= 0, steps 1..100, all finite; scale 0
+ *                stands for 0.2 sqrt(max(rows, cols)), which makes the update as
+ *                large as AdamW's.
+ *   workspace    device, workspace_bytes of it: ep_muon_workspace_bytes (host;
+ *                -1 for sizes that are refused) says how much is of use, at most
+ *                4 GiB or what the largest matrix needs; with less, down to that
+ *                matrix's own need (the answer for a batch of 1), fewer matrices
+ *                go through at once.  Results do not depend on it.
+ * Any rows and cols up to 65536 and 2^29 values of a matrix (else
+ * EP_ERR_UNSUPPORTED); empty tensors are skipped.  Pointers are 16-byte aligned;
+ * a buffer that is written shares memory with no other (EP_ERR_INVALID_ARGUMENT).
+ * X is held in fp16 twice (a value and what its rounding left), the products run
+ * in fp16 with fp32 sums: X is some 1.5e-3 of its norm off.  X must stay below 8
+ * in the 2-norm, and |b| s^2 + |c| s^4 below 60 there, which the coefficients
+ * above do with room to spare; past that results are not finite.  A matrix
+ * of zeros has X = 0; one with an infinity or NaN has a result that is none, and
+ * spoils no other.  Sums are made in a fixed order.
+ * 2 + 3 steps launches for up to 40 tensors as the workspace holds them (one
+ * more with both tall and other matrices); capturable. */
+#define EP_MUON_PARAM_BF16 (1u << 19)
+#define EP_MUON_GRAD_BF16  (1u << 20)
+#define EP_MUON_NESTEROV   (1u << 21)
+typedef struct ep_muon_tensor {
+    void* param;
+    const void* grad;
+    float* momentum;
+    void* copy;
+    int64_t batch;
+    int32_t rows;
+    int32_t cols;
+} ep_muon_tensor;
+typedef struct ep_muon_config {
+    double lr;
+    double momentum;
+    double weight_decay;
+    double scale;
+    double eps;
+    double a;
+    double b;
+    double c;
+    int32_t steps;
+    uint32_t flags;
+} ep_muon_config;
+int64_t ep_muon_workspace_bytes(const ep_muon_tensor* tensors, int32_t count);
+ep_status ep_muon(const ep_muon_tensor* tensors, int32_t count, const ep_muon_config* cfg, void* workspace,
+                  int64_t workspace_bytes, hipStream_t stream);
+
+/* X alone, as ep_muon makes it, of U = x: out (device bf16 [batch, rows, cols])
+ * from x (device fp32, EP_MUON_GRAD_BF16: bf16, the only flag).  coefficients:
+ * a, b, c on the host, or NULL for those above.  Workspace, limits and the rest as for ep_muon. */
+ep_status ep_orthogonalize(const void* x, int64_t batch, int32_t rows, int32_t cols, int32_t steps,
+                           const double coefficients[3], double eps, uint32_t flags, void* workspace,
+                           int64_t workspace_bytes, void* out, hipStream_t stream);
 
 /* End the lease of a borrowing dispatch ([BORROW]).  consumer_stream is the
  * stream the consumers of the view were enqueued on; the handle's next call
