@@ -16,7 +16,11 @@
 // hi and 2^-11 lo: the first steps multiply small singular values by a = 3.4 each, and
 // with them whatever rounding X had; the products see hi alone, where a rounding
 // is no more than its share of P X (matrices of rank 16 in noise-free form:
-// 4e-4 instead of 4.5e-2).
+// 4e-4 instead of 4.5e-2).  In the last two steps X = (a - k) X + (P + k I) X with
+// k = -(b l + c l^2), l the mean of G's diagonal: the same, but where singular values have
+// come near 1 P + k I is small and its rounding with it (noise of 512 x 1792: 9.6e-4
+// before the result's own rounding instead of 1.7e-3).  Earlier it would put the
+// rounding of hi, k times it, among the singular values that are still small.
 //
 // One launch serves all matrices of a list: their shapes and addresses travel
 // in the kernel's arguments.  Step by step: the norms (with the momentum), the
@@ -77,6 +81,8 @@ struct Problem {
     __device__ _Float16* g() const { return (_Float16*)ws + 3 * batch * x_size(); }
     __device__ _Float16* p() const { return (_Float16*)ws + 3 * batch * x_size() + batch * g_size(); }
     __device__ double* sums() const { return (double*)((_Float16*)ws + 3 * batch * x_size() + 2 * batch * g_size()); }
+    // k of the shifted steps, where the sums were (read before)
+    __device__ float& shift(int mat) const { return *(float*)(sums() + (int64_t)mat * partials); }
     // bytes of one matrix; a multiple of 16, since the leading dimensions are multiples of 8
     __host__ int64_t ws_each() const { return 6 * x_size() + 4 * g_size() + (int64_t)partials * 8; }
 };
@@ -84,6 +90,7 @@ struct Problem {
 struct GroupArgs {
     int32_t count;
     int32_t turn;               // which hi is read
+    int32_t shifted;            // one of the last two steps
     int32_t x_bf16, param_bf16, nesterov;
     float a, b, c;
     float mu, rest_mu;          // momentum
@@ -248,10 +255,22 @@ __device__ __forceinline__ void write_results(const GroupArgs& a, const Problem&
     }
 }
 
-// A wave's part of a finished tile: rows from r_at, columns from c_at.
+// k, from G's diagonal, by every wave for itself.
+__device__ __forceinline__ float shift_of(const GroupArgs& a, const Problem& p, int mat, int lane) {
+    const _Float16* const g = p.g() + mat * p.g_size();
+    float sum = 0.0f;
+#pragma unroll 4
+    for (int r = lane; r < p.m; r += kWave) sum += (float)g[(int64_t)r * (p.ld_m + 1)];
+#pragma unroll
+    for (int d = kWave / 2; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
+    const float l = fminf(sum / ((float)p.m * kGramScale), 1.0f);
+    return -(a.b * l + a.c * (l * l));
+}
+
+// A wave's part of a finished tile: rows from r_at, columns from c_at; k: the shift.
 template <class S, int MF, int NF>
 __device__ __forceinline__ void finish(const GroupArgs& a, const Problem& p, int mat, int r_at, int c_at, bool mirror, int lane,
-                                       const f32x4 (&acc)[MF][NF]) {
+                                       float k, const f32x4 (&acc)[MF][NF]) {
     constexpr int OP = S::OP;
     if constexpr (OP == kLastTall) {
         // lane l holds column l % 16; its rows lie together in the result
@@ -270,7 +289,7 @@ __device__ __forceinline__ void finish(const GroupArgs& a, const Problem& p, int
                 for (int q = 0; q < 8; ++q)
                     if (r + q < p.m) {
                         const int64_t from = (int64_t)(r + q) * p.ld_n + c;
-                        v[q] = a.a * ((float)hi[from] + (float)lo[from] * (1.0f / kLow)) + v[q] * (1.0f / kGramScale);
+                        v[q] = (a.a - k) * ((float)hi[from] + (float)lo[from] * (1.0f / kLow)) + v[q] * (1.0f / kGramScale);
                     }
                 write_results(a, p, (int64_t)mat * p.m * p.n + (int64_t)c * p.m + r, p.m - r, v);
             }
@@ -298,7 +317,9 @@ __device__ __forceinline__ void finish(const GroupArgs& a, const Problem& p, int
                         f16x8 old = {0, 0, 0, 0, 0, 0, 0, 0};
                         if (real) old = *(const f16x8*)(g + (int64_t)r * p.ld_m + c);
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) w[q] = (_Float16)(a.b * (float)old[q] + a.c * (v[q] * (1.0f / kGramScale)));
+                        for (int q = 0; q < 8; ++q)
+                            w[q] = (_Float16)(a.b * (float)old[q] + a.c * (v[q] * (1.0f / kGramScale)) +
+                                              (c + q == r && real ? k * kGramScale : 0.0f));
                     }
                     if (real) *(f16x8*)(out + (int64_t)r * p.ld_m + c) = w;
                     if (mirror)
@@ -311,7 +332,7 @@ __device__ __forceinline__ void finish(const GroupArgs& a, const Problem& p, int
                     const f16x8 h = *(const f16x8*)(p.hi(a.turn) + at), l = *(const f16x8*)(p.lo() + at);
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
-                        v[q] = a.a * ((float)h[q] + (float)l[q] * (1.0f / kLow)) + v[q] * (1.0f / kGramScale);
+                        v[q] = (a.a - k) * ((float)h[q] + (float)l[q] * (1.0f / kLow)) + v[q] * (1.0f / kGramScale);
                     if constexpr (OP == kNext) {
                         f16x8 nh, nl;
 #pragma unroll
@@ -385,7 +406,12 @@ __global__ void __launch_bounds__(S::kThreads) muon_gemm_kernel(GroupArgs a) {
         constexpr int kAcross = BN / WN;
         const int r = wave / kAcross * WM, c = wave % kAcross * WN;
         auto done = [&](const f32x4 (&acc)[WM / 16][WN / 16]) {
-            finish<S, WM / 16, WN / 16>(a, p, mat, m0 + r, n0 + c, mt != nt, lane, acc);
+            float k = 0.0f;
+            if (OP != kGram && a.shifted) {
+                k = OP == kPoly ? shift_of(a, p, mat, lane) : p.shift(mat);
+                if (OP == kPoly && in == 0 && tid == 0) p.shift(mat) = k;
+            }
+            finish<S, WM / 16, WN / 16>(a, p, mat, m0 + r, n0 + c, mt != nt, lane, k, acc);
         };
         if constexpr (S::kPipelined) pipelined_tile<S, WM / 16, WN / 16>(la, lb, K, r, c, wave, lane, lds, done);
         else plain_tile<S>(la, lb, K, r, c, wave, lane, lds, done);
@@ -454,6 +480,7 @@ hipError_t run_group(GroupArgs& a, int steps, int num_cu, hipStream_t stream) {
     muon_split_kernel<<<(int)blocks, kThreads, 0, stream>>>(a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     for (int s = 0; s < steps; ++s) {
+        a.shifted = s + 2 >= steps;
         if ((e = launch_product<kGram>(a, num_cu, stream)) != hipSuccess) return e;
         if ((e = launch_product<kPoly>(a, num_cu, stream)) != hipSuccess) return e;
         if (s + 1 < steps) e = launch_product<kNext>(a, num_cu, stream);

@@ -52,12 +52,17 @@ def rounded(x, steps=5, abc=ABC, eps=1e-7):
     x, tall = _wide(x.double())
     s = 2.0 ** round(0.5 * torch.log2(torch.tensor(float(x.shape[-1]))).item())
     x = _start(x, eps)
-    for _ in range(steps):
+    one = torch.eye(x.shape[-2], dtype=torch.float64, device=x.device)
+    for i in range(steps):
         hi = f16(x, s)
         x = hi + f16(x - hi, s * 2048)
         g = f16(hi @ hi.mT.contiguous(), 1024.0)
-        p = f16(b * g + c * (g @ g), 1024.0)
-        x = a * x + p @ hi
+        k = 0.0
+        if i + 2 >= steps:              # the last two steps: P + k I
+            l = g.diagonal(dim1=-2, dim2=-1).mean(-1).clamp_max(1.0)[..., None, None]
+            k = -(b * l + c * l * l)
+        p = f16(b * g + c * (g @ g) + k * one, 1024.0)
+        x = (a - k) * x + p @ hi
     return x.mT if tall else x
 
 
@@ -65,7 +70,9 @@ def near(got, x, steps, abc=ABC, eps=1e-7):
     """fp32 results of one or two steps, matrix by matrix."""
     want = rounded(x, steps, abc, eps)
     before = exact(x, steps - 1, abc, eps) if steps > 1 else exact(x, 0, abc, eps)
-    made = torch.linalg.matrix_norm(want - abc[0] * before)
+    l = (torch.linalg.matrix_norm(before).square() / min(x.shape[-2:])).clamp_max(1.0)
+    k = (abc[1] * l + abc[2] * l * l).abs()
+    made = torch.linalg.matrix_norm(want - abc[0] * before) + k * torch.linalg.matrix_norm(before)
     if steps > 1:               # the first step's flips, too
         made = made + torch.linalg.matrix_norm(want)
     off = torch.linalg.matrix_norm(got.double() - want)
