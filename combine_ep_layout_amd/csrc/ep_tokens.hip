@@ -42,6 +42,7 @@ constexpr int kRows = 16;                   // rows of a matrix that a workgroup
 constexpr int kMaxTokens = 64;
 constexpr int kMaxSlots = kMaxTokens * kRouteMaxTopK;
 constexpr int kMaxExperts = kRouteMaxExperts;
+constexpr int kMaxUsed = kMaxExperts + kMaxSlots / 16;
 constexpr int kMaxWidth = 1 << 16;          // hidden, inter
 constexpr int64_t kMaxMatrix = 1 << 29;     // hidden * inter of one expert
 // An offset past every buffer, also with a row's own offset added: such a lane loads zeros.
@@ -139,16 +140,17 @@ struct Slots {
     int16_t expert[kMaxSlots];              // -1: none
     int16_t rank[kMaxSlots];                // among the expert's slots, -1: none
     float weight[kMaxSlots];
-    int32_t count[kMaxExperts];             // then the expert's first place
-    int16_t used[kMaxExperts];              // experts with a slot, ascending
-    int32_t start[kMaxExperts + 1];         // their first places
+    int32_t count[kMaxExperts];             // then the expert's first place, and its slots << 16
+    int16_t used[kMaxUsed];                 // experts with a slot, ascending
+    int32_t start[kMaxUsed + 1];            // their first places
     int16_t sorted[kMaxSlots];
     int32_t n_used;
-    int32_t most;                           // slots of one expert at most
 };
 
-// ROUTE: the choice is made here, a wave a token.
-template <bool ROUTE>
+// ROUTE: the choice is made here, a wave a token.  CHUNK: an expert with more
+// slots than this is listed several times, the slots in their order (which one
+// is listed where decides which waves share its sums).
+template <bool ROUTE, int CHUNK>
 __device__ __forceinline__ void find_slots(const TokensArgs& a, Slots& s) {
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = uni(tid / kWave);
     const int S = a.T * a.K;
@@ -184,7 +186,7 @@ __device__ __forceinline__ void find_slots(const TokensArgs& a, Slots& s) {
         if (e >= 0) {
             bool first = true;
             for (int j = t * a.K; j < i; ++j) first = first && s.expert[j] != e;
-            if (first) rank = atomicAdd(&s.count[e], 1);        // the order of an expert's slots changes no result
+            if (first) rank = atomicAdd(&s.count[e], 1);        // in any order
         }
         s.rank[i] = (int16_t)rank;
         if (rank >= 0)
@@ -194,44 +196,53 @@ __device__ __forceinline__ void find_slots(const TokensArgs& a, Slots& s) {
     __syncthreads();
     if (wave == 0) {
         const int per = (a.E + kWave - 1) / kWave;
-        int used = 0, slots = 0, most = 0;
+        int used = 0, slots = 0;
 #pragma unroll 1
         for (int i = 0; i < per; ++i) {
             const int e = lane * per + i, n = e < a.E ? s.count[e] : 0;
-            used += n > 0;
+            used += (n + CHUNK - 1) / CHUNK;
             slots += n;
-            most = n > most ? n : most;
         }
-        int before = used << 16 | slots;            // at most 1024 and 2048
+        int before = used << 16 | slots;            // at most kMaxUsed and 2048
 #pragma unroll
         for (int d = 1; d < kWave; d <<= 1) {
             const int o = __shfl_up(before, d);
             if (lane >= d) before += o;
-            const int m = __shfl_xor(most, d);
-            most = m > most ? m : most;
         }
         if (lane == kWave - 1) {
             s.n_used = before >> 16;
             s.start[before >> 16] = before & 0xFFFF;
-            s.most = most;
         }
         before -= used << 16 | slots;
         int u = before >> 16, p = before & 0xFFFF;
 #pragma unroll 1
         for (int i = 0; i < per; ++i) {
             const int e = lane * per + i, n = e < a.E ? s.count[e] : 0;
-            if (n > 0) {
+            if (n > 0) s.count[e] = p | n << 16;
+            for (int k = 0; k < n; k += CHUNK) {
                 s.used[u] = (int16_t)e;
-                s.start[u++] = p;
-                s.count[e] = p;
-                p += n;
+                s.start[u++] = p + k;
             }
+            p += n;
         }
     }
     __syncthreads();
     for (int i = tid; i < S; i += kThreads)
-        if (s.rank[i] >= 0) s.sorted[s.count[s.expert[i]] + s.rank[i]] = (int16_t)i;
+        if (s.rank[i] >= 0) s.sorted[(s.count[s.expert[i]] & 0xFFFF) + s.rank[i]] = (int16_t)i;
     __syncthreads();
+    if constexpr (CHUNK < kMaxTokens) {
+        for (int i = tid; i < S; i += kThreads) {
+            if (s.rank[i] < 0) continue;
+            const int p = s.count[s.expert[i]] & 0xFFFF, n = s.count[s.expert[i]] >> 16;
+            int before = 0;
+            for (int j = p; j < p + n; ++j) before += s.sorted[j] < i;
+            s.rank[i] = (int16_t)before;
+        }
+        __syncthreads();
+        for (int i = tid; i < S; i += kThreads)
+            if (s.rank[i] >= 0) s.sorted[(s.count[s.expert[i]] & 0xFFFF) + s.rank[i]] = (int16_t)i;
+        __syncthreads();
+    }
 }
 
 // What a wave loads for one step: M matrices' parts and NT tiles of 16 tokens.
@@ -269,16 +280,11 @@ __device__ __forceinline__ void multiply(const Stage<W, M, NT>& s, f32x4 (&c)[M]
         }
 }
 
-// Steps that a wave loads ahead.
+// Gate and up rows [tile * 16, + 16) of expert e, for n of the sorted slots.
 template <class W, int NT>
-constexpr int kAhead = NT == 1 ? 4 : NT == 2 ? 3 : 2;
-
-// Gate and up rows [tile * 16, + 16) of the u-th used expert, for its slots.
-template <class W, int NT>
-__device__ __forceinline__ void up_item(const TokensArgs& a, const Slots& s, float* red, int u, int tile) {
-    constexpr int D = kAhead<W, NT>;
+__device__ __forceinline__ void up_item(const TokensArgs& a, const Slots& s, float* red, int e, int first, int n, int tile) {
+    constexpr int D = NT == 1 ? 4 : 2;          // steps that a wave loads ahead
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = uni(tid / kWave), q = lane >> 4;
-    const int e = uni(s.used[u]), first = uni(s.start[u]), n = uni(s.start[u + 1]) - first;
     const int r0 = tile * kRows;
     const typename W::Matrix m[2] = {W::open(a.w_gate_up, a.s_gate_up, e, 2 * (int64_t)a.I, 0, a.I, a.H),
                                      W::open(a.w_gate_up, a.s_gate_up, e, 2 * (int64_t)a.I, a.I, a.I, a.H)};
@@ -300,7 +306,10 @@ __device__ __forceinline__ void up_item(const TokensArgs& a, const Slots& s, flo
         load_stage<W, 2, NT>(stage[slot], m, l, x, x_at, step, a.H - step * W::kStep, q);
     };
 #pragma unroll
-    for (int d = 0; d < D; ++d) load(d, d);
+    for (int d = 0; d < D; ++d) {
+        load(d, d);
+        __builtin_amdgcn_sched_barrier(0);      // in this order, or the loop's first wait would be for all of them
+    }
 #pragma unroll 1
     for (int i = 0; i < mine; i += D) {
 #pragma unroll
@@ -332,27 +341,29 @@ __device__ __forceinline__ void up_item(const TokensArgs& a, const Slots& s, flo
     }
 }
 
-// NT: tiles of 16 tokens that an expert can have.
-template <class W, int NT, bool ROUTE>
+// MANY: an expert may have more than 16 tokens.  Two tiles of them are the most
+// that the registers hold; a third and fourth are another pass over the weights.
+template <class W, bool MANY, bool ROUTE>
 __global__ void __launch_bounds__(kThreads, 4) tokens_up_kernel(TokensArgs a) {
     __shared__ Slots s;
     __shared__ __attribute__((aligned(16))) float red[kWaves * 512];
-    find_slots<ROUTE>(a, s);
+    find_slots<ROUTE, kMaxTokens>(a, s);
     const int tiles = (a.I + kRows - 1) / kRows, items = uni(s.n_used) * tiles;
     for (int i = blockIdx.x; i < items; i += gridDim.x) {
         const int u = i / tiles, tile = i - u * tiles;
-        const int n = uni(s.start[u + 1]) - uni(s.start[u]);
-        if (NT == 1 || n <= 16) up_item<W, 1>(a, s, red, u, tile);
-        else if (NT == 2 || n <= 32) up_item<W, 2>(a, s, red, u, tile);
-        else if constexpr (NT == 4) up_item<W, 4>(a, s, red, u, tile);
+        const int e = uni(s.used[u]), first = uni(s.start[u]), n = uni(s.start[u + 1]) - first;
+        if (!MANY || n <= 16) up_item<W, 1>(a, s, red, e, first, n, tile);
+        else
+            for (int k = 0; k < n; k += 32) up_item<W, 2>(a, s, red, e, first + k, n - k < 32 ? n - k : 32, tile);
     }
 }
 
 // Columns [tile * 16, + 16) of y.  A wave takes an eighth of the used experts'
-// steps, one after another; sums: [wave][token][16].
-template <class W, int NT, int TOKENS>
+// steps, one after another; sums: [wave][token][16].  An expert's further tokens
+// past 16 read its rows again, out of the L2 where they just were.
+template <class W, int TOKENS>
 __device__ __forceinline__ void down_item(const TokensArgs& a, const Slots& s, float (&sums)[kWaves][TOKENS][kRows], int tile) {
-    constexpr int D = kAhead<W, NT>;
+    constexpr int D = 4, NT = 1;
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = uni(tid / kWave), q = lane >> 4;
     const int steps = (a.I + W::kStep - 1) / W::kStep, units = uni(s.n_used) * steps;
     const int begin = (int)((int64_t)units * wave / kWaves), end = (int)((int64_t)units * (wave + 1) / kWaves);
@@ -390,7 +401,10 @@ __device__ __forceinline__ void down_item(const TokensArgs& a, const Slots& s, f
     if (begin < end) {
         open();
 #pragma unroll
-        for (int d = 0; d < D; ++d) load(d, begin + d);
+        for (int d = 0; d < D; ++d) {
+            load(d, begin + d);
+            __builtin_amdgcn_sched_barrier(0);
+        }
 #pragma unroll 1
         for (int i = begin; i < end; i += D) {
 #pragma unroll
@@ -435,49 +449,43 @@ __device__ __forceinline__ void down_item(const TokensArgs& a, const Slots& s, f
     __syncthreads();
 }
 
-template <class W, int NT>
+template <class W, int TOKENS>
 __global__ void __launch_bounds__(kThreads, 4) tokens_down_kernel(TokensArgs a) {
     __shared__ Slots s;
-    __shared__ __attribute__((aligned(16))) float sums[kWaves][NT * 16][kRows];
-    for (int i = threadIdx.x; i < kWaves * NT * 16 * kRows; i += kThreads) (&sums[0][0][0])[i] = 0.f;
-    find_slots<false>(a, s);
-    const int tiles = (a.H + kRows - 1) / kRows, most = uni(s.most);
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        if (NT == 1 || most <= 16) down_item<W, 1>(a, s, sums, tile);
-        else if (NT == 2 || most <= 32) down_item<W, 2>(a, s, sums, tile);
-        else if constexpr (NT == 4) down_item<W, 4>(a, s, sums, tile);
-    }
+    __shared__ __attribute__((aligned(16))) float sums[kWaves][TOKENS][kRows];
+    for (int i = threadIdx.x; i < kWaves * TOKENS * kRows; i += kThreads) (&sums[0][0][0])[i] = 0.f;
+    find_slots<false, TOKENS == 16 ? kMaxTokens : 16>(a, s);        // of 16 tokens no expert has more
+    const int tiles = (a.H + kRows - 1) / kRows;
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) down_item<W, TOKENS>(a, s, sums, tile);
 }
 
 // From so many tokens on, or past 256 experts, the choice has a launch of its own:
 // a workgroup would have to make more than its waves can at once.
 constexpr int kRouteHereTokens = kWaves;
-static_assert(kRouteHereTokens <= 16, "one tile of tokens");
+static_assert(kRouteHereTokens <= 16, "no expert has more");
 constexpr int kRouteHereExperts = 256;
 
-template <class W, int NT>
+template <class W, bool MANY>
 hipError_t launch(const TokensArgs& a, int num_cu, hipStream_t stream) {
     const int most = 2 * num_cu;            // two workgroups of a compute unit
     const int64_t used = (int64_t)a.T * a.K < a.E ? (int64_t)a.T * a.K : a.E;
     const int64_t up = used * ((a.I + kRows - 1) / kRows), down = (a.H + kRows - 1) / kRows;
     const int g1 = (int)(up < most ? up : most), g2 = (int)(down < most ? down : most);
     bool here = false;
-    if constexpr (NT == 1) {
+    if constexpr (!MANY) {
         here = a.route_here;
-        if (here) tokens_up_kernel<W, NT, true><<<g1, kThreads, 0, stream>>>(a);
+        if (here) tokens_up_kernel<W, MANY, true><<<g1, kThreads, 0, stream>>>(a);
     }
-    if (!here) tokens_up_kernel<W, NT, false><<<g1, kThreads, 0, stream>>>(a);
+    if (!here) tokens_up_kernel<W, MANY, false><<<g1, kThreads, 0, stream>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    tokens_down_kernel<W, NT><<<g2, kThreads, 0, stream>>>(a);
+    tokens_down_kernel<W, MANY ? kMaxTokens : 16><<<g2, kThreads, 0, stream>>>(a);
     return hipGetLastError();
 }
 
 template <class W>
 hipError_t launch(const TokensArgs& a, int num_cu, hipStream_t stream) {
-    if (a.T <= 16) return launch<W, 1>(a, num_cu, stream);
-    if (a.T <= 32) return launch<W, 2>(a, num_cu, stream);
-    return launch<W, 4>(a, num_cu, stream);
+    return a.T <= 16 ? launch<W, false>(a, num_cu, stream) : launch<W, true>(a, num_cu, stream);
 }
 
 constexpr uint32_t kRouteFlags = EP_ROUTE_BF16 | EP_ROUTE_SIGMOID | EP_ROUTE_NORMALIZE;
