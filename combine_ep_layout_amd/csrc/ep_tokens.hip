@@ -75,14 +75,16 @@ __device__ __forceinline__ u32x4 load16(Buffer b, uint32_t lane, int at) {
     return __builtin_amdgcn_raw_buffer_load_b128(b, (int)lane, at, 0);
 }
 
-// The weights' forms.  A step is what one 16-byte load of each lane's row covers
-// (bf16: two loads); lane l holds row l % 16 and the summed indices of its
-// quarter q = l / 16, in kFrags fragments of 8.
+// The weights' forms.  A step is 64 (bf16) or 128 (4-bit) summed indices of a
+// row, four steps are a group; lane l holds row l % 16 and the indices of its
+// quarter q = l / 16 in kFrags fragments of 8.  kTiles: row tiles of a wave, which
+// share what is loaded of the tokens: beside 4-bit weights these are as many bytes.
 struct Bf16Weights {
-    static constexpr int kStep = 64, kFrags = 2;
+    static constexpr int kStep = 64, kFrags = 2, kTiles = 1;
     struct Regs { u32x4 v[2]; };
+    struct Scales {};
     struct Matrix { Buffer w; };
-    // rows x n of expert e, from row `first`
+    // rows x n of expert e, from row `first` of each
     __device__ static Matrix open(const void* w, const uint8_t*, int64_t e, int64_t each, int64_t first, int64_t rows, int n) {
         return {buffer((const __bf16*)w + (e * each + first) * n, rows * n * 2)};
     }
@@ -99,37 +101,64 @@ struct Bf16Weights {
         for (int f = 0; f < 2; ++f) r.v[f] = load16(m.w, k_of(q, f) < left ? l.at + f * 64 : kOutOfRange, step * (kStep * 2));
         return r;
     }
-    __device__ static bf16x8 fragment(const Regs& r, int f) { return __builtin_bit_cast(bf16x8, r.v[f]); }
+    __device__ static Scales load_scales(const Matrix&, const Lane&, int, int) { return {}; }
+    __device__ static void settle(Scales&) {}
+    __device__ static float scale_of(const Scales&, const Lane&, int, int, int) { return 1.0f; }
+    __device__ static bf16x8 fragment(const Regs& r, float, int f) {
+        return __builtin_bit_cast(bf16x8, r.v[f]);
+    }
 };
 
 struct Mxfp4Weights {
-    static constexpr int kStep = 128, kFrags = 4;
-    struct Regs { u32x4 v; uint32_t scale; };
-    struct Matrix { Buffer w, s; };
+    static constexpr int kStep = 128, kFrags = 4, kTiles = 2;
+    struct Regs { u32x4 v; };
+    // a row's bytes of a group: four of each step (one for each quarter)
+    struct Scales { u32x4 v; uint32_t more; int over; };
+    struct Matrix { Buffer w, s; int bytes; };
     __device__ static Matrix open(const void* w, const uint8_t* s, int64_t e, int64_t each, int64_t first, int64_t rows, int n) {
         const int64_t at = e * each + first;
-        return {buffer((const uint8_t*)w + at * (n / 2), rows * (n / 2)), buffer(s + at * (n / 32), rows * (n / 32))};
+        return {buffer((const uint8_t*)w + at * (n / 2), rows * (n / 2)), buffer(s + at * (n / 32), rows * (n / 32)),
+                (int)(rows * (n / 32))};
     }
     __device__ static int k_of(int q, int f) { return q * 32 + f * 8; }
-    struct Lane { uint32_t at, scale; };
+    struct Lane { uint32_t at, scale, shift; };
     __device__ static Lane lane(int row, int rows, int n, int q) {
-        return row < rows ? Lane{(uint32_t)row * (uint32_t)(n / 2) + q * 16, (uint32_t)row * (uint32_t)(n / 32) + q}
-                          : Lane{kOutOfRange, kOutOfRange};
+        const uint32_t s = (uint32_t)row * (uint32_t)(n / 32);
+        return row < rows ? Lane{(uint32_t)row * (uint32_t)(n / 2) + q * 16, s & ~3u, s & 3u} : Lane{kOutOfRange, kOutOfRange, 0};
     }
     __device__ static Regs load(const Matrix& m, const Lane& l, int step, int left, int q) {
-        const bool in = q * 32 < left;
-        Regs r;
-        r.v = load16(m.w, in ? l.at : kOutOfRange, step * (kStep / 2));
-        r.scale = __builtin_amdgcn_raw_buffer_load_b8(m.s, (int)(in ? l.scale : kOutOfRange), step * (kStep / 32), 0);
-        return r;
+        return {load16(m.w, q * 32 < left ? l.at : kOutOfRange, step * (kStep / 2))};
     }
-    __device__ static bf16x8 fragment(const Regs& r, int f) {
-        const float s = __uint_as_float(r.scale << 23);
+    // 16 bytes from the row's dword on, for rows that start inside a dword 4 more.
+    // A matrix has a multiple of 32 bytes; its last row's last load comes from
+    // further up instead of reaching past them, by `over` (4, 8 or 12).
+    __device__ static Scales load_scales(const Matrix& m, const Lane& l, int step, int n) {
+        Scales s;
+        const uint32_t at = l.scale + (uint32_t)step * 4;
+        const bool in = l.scale != kOutOfRange && at < (uint32_t)m.bytes;
+        s.over = in && at + 16 > (uint32_t)m.bytes ? (int)(at + 16 - (uint32_t)m.bytes) : 0;
+        s.v = load16(m.s, in ? at - s.over : kOutOfRange, 0);
+        s.more = 0;
+        if ((n & 127) != 0) s.more = __builtin_amdgcn_raw_buffer_load_b32(m.s, (int)(in ? at + 16 : kOutOfRange), 0, 0);
+        return s;
+    }
+    // ready to be used: the words where they belong
+    __device__ static void settle(Scales& s) {
+        if (__ballot(s.over != 0) == 0) return;
+        if (s.over & 4) s.v = u32x4{s.v[1], s.v[2], s.v[3], 0};
+        if (s.over & 8) s.v = u32x4{s.v[2], s.v[3], 0, 0};
+    }
+    // d: the step inside its group.  A byte past the row may be anything.
+    __device__ static float scale_of(const Scales& s, const Lane& l, int d, int left, int q) {
+        const uint32_t four = __builtin_amdgcn_alignbyte(d < 3 ? s.v[d < 3 ? d + 1 : 3] : s.more, s.v[d], l.shift);
+        return __uint_as_float(q * 32 < left ? (four >> (8 * q) & 0xFFu) << 23 : 0u);
+    }
+    __device__ static bf16x8 fragment(const Regs& r, float scale, int f) {
         union { bf16x2 p[4]; bf16x8 v; } u;
-        u.p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r.v[f], s, 0);
-        u.p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r.v[f], s, 1);
-        u.p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r.v[f], s, 2);
-        u.p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r.v[f], s, 3);
+        u.p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r.v[f], scale, 0);
+        u.p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r.v[f], scale, 1);
+        u.p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r.v[f], scale, 2);
+        u.p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r.v[f], scale, 3);
         return u.v;
     }
 };
@@ -245,50 +274,79 @@ __device__ __forceinline__ void find_slots(const TokensArgs& a, Slots& s) {
     }
 }
 
-// What a wave loads for one step: M matrices' parts and NT tiles of 16 tokens.
+// What a wave loads for one step: M parts of matrices and NT tiles of 16 tokens.
 template <class W, int M, int NT>
 struct Stage {
     typename W::Regs w[M];
     u32x4 x[NT][W::kFrags];
 };
 
-// x_at: the lane's token's offset in bytes, or kOutOfRange.
-template <class W, int M, int NT>
-__device__ __forceinline__ void load_stage(Stage<W, M, NT>& s, const typename W::Matrix (&m)[M], const typename W::Lane& l,
-                                           Buffer x, const uint32_t (&x_at)[NT], int step, int left, int q) {
-    // The buffers' range is checked less the common offset, which therefore stays inside.
-    step = left > 0 ? step : 0;
-#pragma unroll
-    for (int i = 0; i < M; ++i) s.w[i] = W::load(m[i], l, step, left, q);
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int f = 0; f < W::kFrags; ++f)
-            s.x[j][f] = load16(x, W::k_of(q, f) < left ? x_at[j] + W::k_of(q, f) * 2 : kOutOfRange, step * (W::kStep * 2));
-}
+// A wave's stream of steps, D of them loaded ahead and the group's scales one
+// group ahead.  S says what a step is: the matrices and lanes, and the tokens' rows.
+template <class W, int M, int NT, int D>
+struct Stream {
+    static_assert(4 % D == 0, "a group is four steps");
+    Stage<W, M, NT> stage[D];
+    typename W::Scales scales[M], ahead[M];
 
-template <class W, int M, int NT>
-__device__ __forceinline__ void multiply(const Stage<W, M, NT>& s, f32x4 (&c)[M][NT]) {
+    // x_at: the lane's token's offset in bytes, or kOutOfRange.  left <= 0: nothing (every lane out of range).
+    __device__ __forceinline__ void load(int d, const typename W::Matrix (&m)[M], const typename W::Lane (&l)[M], Buffer x,
+                                         const uint32_t (&x_at)[NT], int step, int left, int q) {
+        Stage<W, M, NT>& s = stage[d % D];
+        // The buffers' range is checked less the common offset, which therefore stays inside.
+        step = left > 0 ? step : 0;
 #pragma unroll
-    for (int f = 0; f < W::kFrags; ++f)
+        for (int i = 0; i < M; ++i) s.w[i] = W::load(m[i], l[i], step, left, q);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int f = 0; f < W::kFrags; ++f)
+                s.x[j][f] = load16(x, W::k_of(q, f) < left ? x_at[j] + W::k_of(q, f) * 2 : kOutOfRange, step * (W::kStep * 2));
+        __builtin_amdgcn_sched_barrier(0);      // in this order, or the first wait in a loop would be for all of them
+    }
+    __device__ __forceinline__ void load_scales(const typename W::Matrix (&m)[M], const typename W::Lane (&l)[M], int step, int n) {
+#pragma unroll
+        for (int i = 0; i < M; ++i) ahead[i] = W::load_scales(m[i], l[i], step, n);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    __device__ __forceinline__ void next_group() {
 #pragma unroll
         for (int i = 0; i < M; ++i) {
-            const bf16x8 w = W::fragment(s.w[i], f);
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-                c[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, s.x[j][f]), c[i][j], 0, 0, 0);
+            scales[i] = ahead[i];
+            W::settle(scales[i]);
         }
-}
+    }
+    __device__ __forceinline__ void multiply(int d, const typename W::Lane (&l)[M], int left, int q, f32x4 (&c)[M][NT]) const {
+        const Stage<W, M, NT>& s = stage[d % D];
+        float scale[M];
+#pragma unroll
+        for (int i = 0; i < M; ++i) scale[i] = W::scale_of(scales[i], l[i], d, left, q);
+#pragma unroll
+        for (int f = 0; f < W::kFrags; ++f)
+#pragma unroll
+            for (int i = 0; i < M; ++i) {
+                const bf16x8 w = W::fragment(s.w[i], scale[i], f);
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    c[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, s.x[j][f]), c[i][j], 0, 0, 0);
+            }
+    }
+};
 
-// Gate and up rows [tile * 16, + 16) of expert e, for n of the sorted slots.
+// Gate and up rows of kTiles row tiles from r0 on, of expert e, for n of the sorted slots.
 template <class W, int NT>
-__device__ __forceinline__ void up_item(const TokensArgs& a, const Slots& s, float* red, int e, int first, int n, int tile) {
-    constexpr int D = NT == 1 ? 4 : 2;          // steps that a wave loads ahead
+__device__ __forceinline__ void up_item(const TokensArgs& a, const Slots& s, float* red, int e, int first, int n, int r0) {
+    constexpr int D = NT == 1 ? 4 : 2, R = W::kTiles, M = 2 * R;
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = uni(tid / kWave), q = lane >> 4;
-    const int r0 = tile * kRows;
-    const typename W::Matrix m[2] = {W::open(a.w_gate_up, a.s_gate_up, e, 2 * (int64_t)a.I, 0, a.I, a.H),
-                                     W::open(a.w_gate_up, a.s_gate_up, e, 2 * (int64_t)a.I, a.I, a.I, a.H)};
-    const typename W::Lane l = W::lane(r0 + (lane & 15), a.I, a.H, q);
+    const typename W::Matrix gate = W::open(a.w_gate_up, a.s_gate_up, e, 2 * (int64_t)a.I, 0, a.I, a.H);
+    const typename W::Matrix up = W::open(a.w_gate_up, a.s_gate_up, e, 2 * (int64_t)a.I, a.I, a.I, a.H);
+    typename W::Matrix m[M];
+    typename W::Lane l[M];
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+        m[i] = i & 1 ? up : gate;
+        l[i] = W::lane(r0 + (i >> 1) * kRows + (lane & 15), a.I, a.H, q);
+    }
     const Buffer x = buffer(a.x, ((int64_t)(a.T - 1) * a.x_ld + a.H) * 2);
     uint32_t x_at[NT];
 #pragma unroll
@@ -296,167 +354,168 @@ __device__ __forceinline__ void up_item(const TokensArgs& a, const Slots& s, flo
         const int i = j * 16 + (lane & 15);
         x_at[j] = i < n ? (uint32_t)(s.sorted[first + i] / a.K) * (uint32_t)a.x_ld * 2u : kOutOfRange;
     }
-    const int steps = (a.H + W::kStep - 1) / W::kStep, mine = (steps - wave + kWaves - 1) / kWaves;
-    f32x4 c[2][NT];
+    // an eighth of the steps, one after another
+    const int steps = (a.H + W::kStep - 1) / W::kStep, begin = steps * wave / kWaves, end = steps * (wave + 1) / kWaves;
+    f32x4 c[M][NT];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) c[0][j] = c[1][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    Stage<W, 2, NT> stage[D];
-    auto load = [&](int slot, int i) {
-        const int step = wave + i * kWaves;
-        load_stage<W, 2, NT>(stage[slot], m, l, x, x_at, step, a.H - step * W::kStep, q);
-    };
+    for (int i = 0; i < M; ++i)
 #pragma unroll
-    for (int d = 0; d < D; ++d) {
-        load(d, d);
-        __builtin_amdgcn_sched_barrier(0);      // in this order, or the loop's first wait would be for all of them
-    }
+        for (int j = 0; j < NT; ++j) c[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    Stream<W, M, NT, D> stream;
+    auto left = [&](int i) { return i < end ? a.H - i * W::kStep : 0; };
+    if (begin < end) {
+        stream.load_scales(m, l, begin, a.H);
+#pragma unroll
+        for (int d = 0; d < D; ++d) stream.load(d, m, l, x, x_at, begin + d, left(begin + d), q);
 #pragma unroll 1
-    for (int i = 0; i < mine; i += D) {
+        for (int i = begin; i < end; i += 4) {
+            stream.next_group();
+            stream.load_scales(m, l, i + 4 < end ? i + 4 : i, a.H);
 #pragma unroll
-        for (int d = 0; d < D; ++d) {
-            multiply<W, 2, NT>(stage[d], c);
-            load(d, i + d + D);
-            __builtin_amdgcn_sched_barrier(0);
+            for (int d = 0; d < 4; ++d) {
+                stream.multiply(d, l, left(i + d), q, c);
+                stream.load(d, m, l, x, x_at, i + d + D, left(i + d + D), q);
+            }
         }
     }
     // lane l holds rows 4 (l / 16) + 0..3 of its slot l % 16
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        if (j * 16 >= n) break;
-        f32x4* const to = (f32x4*)red + wave * 128 + lane;
-        to[0] = c[0][j];
-        to[64] = c[1][j];
-        __syncthreads();
-        if (tid < 256) {
-            float g = 0.f, up = 0.f;
+    for (int t = 0; t < R; ++t)
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w) {
-                g += red[w * 512 + tid];
-                up += red[w * 512 + 256 + tid];
+        for (int j = 0; j < NT; ++j) {
+            if (j * 16 >= n) break;
+            f32x4* const to = (f32x4*)red + wave * 128 + lane;
+            to[0] = c[2 * t][j];
+            to[64] = c[2 * t + 1][j];
+            __syncthreads();
+            if (tid < 256) {
+                float g = 0.f, u = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) {
+                    g += red[w * 512 + tid];
+                    u += red[w * 512 + 256 + tid];
+                }
+                const int i = j * 16 + ((tid >> 2) & 15), r = r0 + t * kRows + (tid >> 6) * 4 + (tid & 3);
+                if (i < n && r < a.I) a.a[(int64_t)s.sorted[first + i] * a.I + r] = (__bf16)(act_value(g, a.act) * u);
             }
-            const int i = j * 16 + ((tid >> 2) & 15), r = r0 + (tid >> 6) * 4 + (tid & 3);
-            if (i < n && r < a.I) a.a[(int64_t)s.sorted[first + i] * a.I + r] = (__bf16)(act_value(g, a.act) * up);
+            __syncthreads();
         }
-        __syncthreads();
-    }
 }
 
 // MANY: an expert may have more than 16 tokens.  Two tiles of them are the most
 // that the registers hold; a third and fourth are another pass over the weights.
 template <class W, bool MANY, bool ROUTE>
-__global__ void __launch_bounds__(kThreads, 4) tokens_up_kernel(TokensArgs a) {
+__global__ void __launch_bounds__(kThreads, 4 / W::kTiles) tokens_up_kernel(TokensArgs a) {
     __shared__ Slots s;
     __shared__ __attribute__((aligned(16))) float red[kWaves * 512];
     find_slots<ROUTE, kMaxTokens>(a, s);
-    const int tiles = (a.I + kRows - 1) / kRows, items = uni(s.n_used) * tiles;
+    constexpr int kSide = W::kTiles * kRows;
+    const int tiles = (a.I + kSide - 1) / kSide, items = uni(s.n_used) * tiles;
     for (int i = blockIdx.x; i < items; i += gridDim.x) {
         const int u = i / tiles, tile = i - u * tiles;
         const int e = uni(s.used[u]), first = uni(s.start[u]), n = uni(s.start[u + 1]) - first;
-        if (!MANY || n <= 16) up_item<W, 1>(a, s, red, e, first, n, tile);
+        if (!MANY || n <= 16) up_item<W, 1>(a, s, red, e, first, n, tile * kSide);
         else
-            for (int k = 0; k < n; k += 32) up_item<W, 2>(a, s, red, e, first + k, n - k < 32 ? n - k : 32, tile);
+            for (int k = 0; k < n; k += 32) up_item<W, 2>(a, s, red, e, first + k, n - k < 32 ? n - k : 32, tile * kSide);
     }
 }
 
-// Columns [tile * 16, + 16) of y.  A wave takes an eighth of the used experts'
-// steps, one after another; sums: [wave][token][16].  An expert's further tokens
-// past 16 read its rows again, out of the L2 where they just were.
+// kTiles * 16 columns of y from c0 on.  A wave takes an eighth of the used experts'
+// groups, one after another; sums: [wave][token][columns].  An expert's further
+// tokens past 16 read its rows again, out of the L2 where they just were.
 template <class W, int TOKENS>
-__device__ __forceinline__ void down_item(const TokensArgs& a, const Slots& s, float (&sums)[kWaves][TOKENS][kRows], int tile) {
-    constexpr int D = 4, NT = 1;
+__device__ __forceinline__ void down_item(const TokensArgs& a, const Slots& s, float (&sums)[kWaves][TOKENS][W::kTiles * kRows], int c0) {
+    constexpr int D = 4, M = W::kTiles, kSide = M * kRows;
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = uni(tid / kWave), q = lane >> 4;
-    const int steps = (a.I + W::kStep - 1) / W::kStep, units = uni(s.n_used) * steps;
+    const int groups = (a.I + 4 * W::kStep - 1) / (4 * W::kStep), units = uni(s.n_used) * groups;
     const int begin = (int)((int64_t)units * wave / kWaves), end = (int)((int64_t)units * (wave + 1) / kWaves);
-    const typename W::Lane l = W::lane(tile * kRows + (lane & 15), a.H, a.I, q);
+    typename W::Lane l[M];
+#pragma unroll
+    for (int i = 0; i < M; ++i) l[i] = W::lane(c0 + i * kRows + (lane & 15), a.H, a.I, q);
     const Buffer x = buffer(a.a, (int64_t)a.T * a.K * a.I * 2);
-    Stage<W, 1, NT> stage[D];
-    f32x4 c[1][NT];
+    Stream<W, M, 1, D> stream;
+    f32x4 c[M][1];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) c[0][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    // where the loads are, and where the products are
-    int load_u = begin / steps, load_step = begin - load_u * steps;
-    int u = load_u, step = load_step;
-    typename W::Matrix m[1] = {};
-    uint32_t x_at[NT];
-    auto open = [&] {
-        const int e = uni(s.used[load_u]), first = uni(s.start[load_u]), n = uni(s.start[load_u + 1]) - first;
-        m[0] = W::open(a.w_down, a.s_down, e, a.H, 0, a.H, a.I);
+    for (int i = 0; i < M; ++i) c[i][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+    typename W::Matrix m[M] = {};
+    uint32_t x_at[1];
+    auto open = [&](int u) {
+        const int e = uni(s.used[u]), first = uni(s.start[u]), n = uni(s.start[u + 1]) - first;
+        const typename W::Matrix w = W::open(a.w_down, a.s_down, e, a.H, 0, a.H, a.I);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const int i = j * 16 + (lane & 15);
-            x_at[j] = i < n ? (uint32_t)s.sorted[first + i] * (uint32_t)a.I * 2u : kOutOfRange;
-        }
-    };
-    auto load = [&](int slot, int i) {
-        // past the wave's last step: nothing (every lane out of range)
-        load_stage<W, 1, NT>(stage[slot], m, l, x, x_at, load_step, i < end ? a.I - load_step * W::kStep : 0, q);
-        if (++load_step == steps) {
-            load_step = 0;
-            if (i + 1 < end) {
-                ++load_u;
-                open();
-            }
-        }
+        for (int i = 0; i < M; ++i) m[i] = w;
+        const int k = lane & 15;
+        x_at[0] = k < n ? (uint32_t)s.sorted[first + k] * (uint32_t)a.I * 2u : kOutOfRange;
     };
     if (begin < end) {
-        open();
+        int u = begin / groups, g = begin - u * groups;         // where the products are
+        open(u);
+        stream.load_scales(m, l, g * 4, a.I);
 #pragma unroll
-        for (int d = 0; d < D; ++d) {
-            load(d, begin + d);
-            __builtin_amdgcn_sched_barrier(0);
-        }
+        for (int d = 0; d < 4; ++d) stream.load(d, m, l, x, x_at, g * 4 + d, a.I - (g * 4 + d) * W::kStep, q);
 #pragma unroll 1
-        for (int i = begin; i < end; i += D) {
+        for (int i = begin; i < end; ++i) {
+            // the next group: of this expert, or of the next one
+            const bool more = i + 1 < end;
+            const int next_g = g + 1 == groups ? 0 : g + 1;
+            if (more && next_g == 0) open(u + 1);
+            stream.next_group();
+            stream.load_scales(m, l, more ? next_g * 4 : 0, a.I);
 #pragma unroll
-            for (int d = 0; d < D; ++d) {
-                multiply<W, 1, NT>(stage[d], c);
-                load(d, i + d + D);
-                __builtin_amdgcn_sched_barrier(0);
-                if (i + d < end && (++step == steps || i + d + 1 == end)) {
-                    // the expert's part is done: every token has it once
-                    const int first = uni(s.start[u]), n = uni(s.start[u + 1]) - first;
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        const int k = j * 16 + (lane & 15);
-                        if (k < n) {
-                            const int slot = s.sorted[first + k];
-                            const float w = s.weight[slot];
-                            f32x4* const to = (f32x4*)&sums[wave][slot / a.K][q * 4];
-                            f32x4 v = *to;
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(w, c[0][j][r], v[r]);
-                            *to = v;
-                        }
-                        c[0][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-                    }
-                    step = 0;
-                    ++u;
-                }
+            for (int d = 0; d < 4; ++d) {
+                stream.multiply(d, l, a.I - (g * 4 + d) * W::kStep, q, c);
+                stream.load(d, m, l, x, x_at, next_g * 4 + d, more ? a.I - (next_g * 4 + d) * W::kStep : 0, q);
             }
+            if (next_g == 0 || !more) {
+                // the expert's part is done: every token has it once
+                const int first = uni(s.start[u]), n = uni(s.start[u + 1]) - first, k = lane & 15;
+                if (k < n) {
+                    const int slot = s.sorted[first + k];
+                    const float w = s.weight[slot];
+#pragma unroll
+                    for (int t = 0; t < M; ++t) {
+                        f32x4* const to = (f32x4*)&sums[wave][slot / a.K][t * kRows + q * 4];
+                        f32x4 v = *to;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(w, c[t][0][r], v[r]);
+                        *to = v;
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < M; ++t) c[t][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+                ++u;
+            }
+            g = next_g;
         }
     }
     __syncthreads();
-    for (int i = tid; i < a.T * kRows; i += kThreads) {
-        const int t = i / kRows, r = i & (kRows - 1);
+    for (int i = tid; i < a.T * kSide; i += kThreads) {
+        const int t = i / kSide, r = i % kSide;
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
             v += sums[w][t][r];
             sums[w][t][r] = 0.f;
         }
-        if (tile * kRows + r < a.H) a.y[(int64_t)t * a.H + tile * kRows + r] = (__bf16)v;
+        if (c0 + r < a.H) a.y[(int64_t)t * a.H + c0 + r] = (__bf16)v;
     }
     __syncthreads();
 }
 
+// The sums follow the slots: past 64 KiB together with 4-bit weights and many tokens.
 template <class W, int TOKENS>
-__global__ void __launch_bounds__(kThreads, 4) tokens_down_kernel(TokensArgs a) {
-    __shared__ Slots s;
-    __shared__ __attribute__((aligned(16))) float sums[kWaves][TOKENS][kRows];
-    for (int i = threadIdx.x; i < kWaves * TOKENS * kRows; i += kThreads) (&sums[0][0][0])[i] = 0.f;
+constexpr size_t kDownLds = sizeof(Slots) / 16 * 16 + 16 + sizeof(float) * kWaves * TOKENS * W::kTiles * kRows;
+
+template <class W, int TOKENS>
+__global__ void __launch_bounds__(kThreads, 4 / W::kTiles) tokens_down_kernel(TokensArgs a) {
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    constexpr int kSide = W::kTiles * kRows;
+    Slots& s = *(Slots*)smem;
+    float (&sums)[kWaves][TOKENS][kSide] = *(float (*)[kWaves][TOKENS][kSide])(smem + sizeof(Slots) / 16 * 16 + 16);
+    for (int i = threadIdx.x; i < kWaves * TOKENS * kSide; i += kThreads) (&sums[0][0][0])[i] = 0.f;
     find_slots<false, TOKENS == 16 ? kMaxTokens : 16>(a, s);        // of 16 tokens no expert has more
-    const int tiles = (a.H + kRows - 1) / kRows;
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) down_item<W, TOKENS>(a, s, sums, tile);
+    const int tiles = (a.H + kSide - 1) / kSide;
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) down_item<W, TOKENS>(a, s, sums, tile * kSide);
 }
 
 // From so many tokens on, or past 256 experts, the choice has a launch of its own:
@@ -467,9 +526,10 @@ constexpr int kRouteHereExperts = 256;
 
 template <class W, bool MANY>
 hipError_t launch(const TokensArgs& a, int num_cu, hipStream_t stream) {
-    const int most = 2 * num_cu;            // two workgroups of a compute unit
+    constexpr int kSide = W::kTiles * kRows, kTokens = MANY ? kMaxTokens : 16;
+    const int most = 2 / W::kTiles * num_cu;            // what the registers let run at once
     const int64_t used = (int64_t)a.T * a.K < a.E ? (int64_t)a.T * a.K : a.E;
-    const int64_t up = used * ((a.I + kRows - 1) / kRows), down = (a.H + kRows - 1) / kRows;
+    const int64_t up = used * ((a.I + kSide - 1) / kSide), down = (a.H + kSide - 1) / kSide;
     const int g1 = (int)(up < most ? up : most), g2 = (int)(down < most ? down : most);
     bool here = false;
     if constexpr (!MANY) {
@@ -479,7 +539,11 @@ hipError_t launch(const TokensArgs& a, int num_cu, hipStream_t stream) {
     if (!here) tokens_up_kernel<W, MANY, false><<<g1, kThreads, 0, stream>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    tokens_down_kernel<W, MANY ? kMaxTokens : 16><<<g2, kThreads, 0, stream>>>(a);
+    constexpr size_t lds = kDownLds<W, kTokens>;
+    if (lds > 64 * 1024 && (e = hipFuncSetAttribute((const void*)tokens_down_kernel<W, kTokens>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                                    (int)lds)) != hipSuccess)
+        return e;
+    tokens_down_kernel<W, kTokens><<<g2, kThreads, lds, stream>>>(a);
     return hipGetLastError();
 }
 
