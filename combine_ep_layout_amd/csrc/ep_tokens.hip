@@ -77,10 +77,14 @@ __device__ __forceinline__ u32x4 load16(Buffer b, uint32_t lane, int at) {
 
 // The weights' forms.  A step is 64 (bf16) or 128 (4-bit) summed indices of a
 // row, four steps are a group; lane l holds row l % 16 and the indices of its
-// quarter q = l / 16 in kFrags fragments of 8.  kTiles: row tiles of a wave, which
-// share what is loaded of the tokens: beside 4-bit weights these are as many bytes.
+// quarter q = l / 16 in kFrags fragments of 8.
+// kUpTiles: row tiles of a wave in the gate and up products.  Two share what is
+// loaded of the tokens, which beside 4-bit weights is as many bytes as the
+// weights (64 tokens: 278 us, 338 with one); beside bf16 weights it is little, and
+// two workgroups of a compute unit that hide each other's ends are worth more
+// (24 experts of 2056 x 1000: 38 us, 43).  kUpWaves: waves of a SIMD so.
 struct Bf16Weights {
-    static constexpr int kStep = 64, kFrags = 2, kTiles = 1;
+    static constexpr int kStep = 64, kFrags = 2, kUpTiles = 1, kUpWaves = 4;
     struct Regs { u32x4 v[2]; };
     struct Scales {};
     struct Matrix { Buffer w; };
@@ -110,7 +114,7 @@ struct Bf16Weights {
 };
 
 struct Mxfp4Weights {
-    static constexpr int kStep = 128, kFrags = 4, kTiles = 2;
+    static constexpr int kStep = 128, kFrags = 4, kUpTiles = 2, kUpWaves = 2;
     struct Regs { u32x4 v; };
     // a row's bytes of a group: four of each step (one for each quarter)
     struct Scales { u32x4 v; uint32_t more; int over; };
@@ -333,44 +337,59 @@ struct Stream {
     }
 };
 
-// Gate and up rows of kTiles row tiles from r0 on, of expert e, for n of the sorted slots.
-template <class W, int NT>
-__device__ __forceinline__ void up_item(const TokensArgs& a, const Slots& s, float* red, int e, int first, int n, int r0) {
-    constexpr int D = NT == 1 ? 4 : 2, R = W::kTiles, M = 2 * R;
-    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = uni(tid / kWave), q = lane >> 4;
-    const typename W::Matrix gate = W::open(a.w_gate_up, a.s_gate_up, e, 2 * (int64_t)a.I, 0, a.I, a.H);
-    const typename W::Matrix up = W::open(a.w_gate_up, a.s_gate_up, e, 2 * (int64_t)a.I, a.I, a.I, a.H);
+// R row tiles of gate and up rows from r0 on, of expert e, for n of the sorted slots.
+struct UpItem {
+    int e, first, n, r0;
+};
+
+// A wave's share of an item: an eighth of the summed index.
+template <class W, int R, int NT>
+struct UpShare {
+    static constexpr int D = NT == 1 ? 4 : 2, M = 2 * R;
     typename W::Matrix m[M];
     typename W::Lane l[M];
-#pragma unroll
-    for (int i = 0; i < M; ++i) {
-        m[i] = i & 1 ? up : gate;
-        l[i] = W::lane(r0 + (i >> 1) * kRows + (lane & 15), a.I, a.H, q);
-    }
-    const Buffer x = buffer(a.x, ((int64_t)(a.T - 1) * a.x_ld + a.H) * 2);
     uint32_t x_at[NT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        const int i = j * 16 + (lane & 15);
-        x_at[j] = i < n ? (uint32_t)(s.sorted[first + i] / a.K) * (uint32_t)a.x_ld * 2u : kOutOfRange;
-    }
-    // an eighth of the steps, one after another
-    const int steps = (a.H + W::kStep - 1) / W::kStep, begin = steps * wave / kWaves, end = steps * (wave + 1) / kWaves;
-    f32x4 c[M][NT];
-#pragma unroll
-    for (int i = 0; i < M; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) c[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    Buffer x;
+    int begin, end, H;
     Stream<W, M, NT, D> stream;
-    auto left = [&](int i) { return i < end ? a.H - i * W::kStep : 0; };
-    if (begin < end) {
-        stream.load_scales(m, l, begin, a.H);
+
+    __device__ __forceinline__ int left(int i) const { return i < end ? H - i * W::kStep : 0; }
+
+    // Puts the first steps' loads on their way.
+    __device__ __forceinline__ void start(const TokensArgs& a, const Slots& s, const UpItem& t, int wave, int lane) {
+        const int q = lane >> 4;
+        const typename W::Matrix gate = W::open(a.w_gate_up, a.s_gate_up, t.e, 2 * (int64_t)a.I, 0, a.I, a.H);
+        const typename W::Matrix up = W::open(a.w_gate_up, a.s_gate_up, t.e, 2 * (int64_t)a.I, a.I, a.I, a.H);
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            m[i] = i & 1 ? up : gate;
+            l[i] = W::lane(t.r0 + (i >> 1) * kRows + (lane & 15), a.I, a.H, q);
+        }
+        x = buffer(a.x, ((int64_t)(a.T - 1) * a.x_ld + a.H) * 2);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const int i = j * 16 + (lane & 15);
+            x_at[j] = i < t.n ? (uint32_t)(s.sorted[t.first + i] / a.K) * (uint32_t)a.x_ld * 2u : kOutOfRange;
+        }
+        H = a.H;
+        const int steps = (H + W::kStep - 1) / W::kStep;
+        begin = steps * wave / kWaves;
+        end = steps * (wave + 1) / kWaves;
+        if (begin == end) return;
+        stream.load_scales(m, l, begin, H);
 #pragma unroll
         for (int d = 0; d < D; ++d) stream.load(d, m, l, x, x_at, begin + d, left(begin + d), q);
+    }
+    __device__ __forceinline__ void run(int lane, f32x4 (&c)[M][NT]) {
+        const int q = lane >> 4;
+#pragma unroll
+        for (int i = 0; i < M; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) c[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
         for (int i = begin; i < end; i += 4) {
             stream.next_group();
-            stream.load_scales(m, l, i + 4 < end ? i + 4 : i, a.H);
+            stream.load_scales(m, l, i + 4 < end ? i + 4 : i, H);
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
                 stream.multiply(d, l, left(i + d), q, c);
@@ -378,15 +397,22 @@ __device__ __forceinline__ void up_item(const TokensArgs& a, const Slots& s, flo
             }
         }
     }
+};
+
+// The waves' sums, the activation and the store of an item.
+template <int R, int NT>
+__device__ __forceinline__ void up_finish(const TokensArgs& a, const Slots& s, float* red, const UpItem& t, int wave, int lane,
+                                          const f32x4 (&c)[2 * R][NT]) {
+    const int tid = threadIdx.x;
     // lane l holds rows 4 (l / 16) + 0..3 of its slot l % 16
 #pragma unroll
-    for (int t = 0; t < R; ++t)
+    for (int k = 0; k < R; ++k)
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            if (j * 16 >= n) break;
+            if (j * 16 >= t.n) break;
             f32x4* const to = (f32x4*)red + wave * 128 + lane;
-            to[0] = c[2 * t][j];
-            to[64] = c[2 * t + 1][j];
+            to[0] = c[2 * k][j];
+            to[64] = c[2 * k + 1][j];
             __syncthreads();
             if (tid < 256) {
                 float g = 0.f, u = 0.f;
@@ -395,37 +421,47 @@ __device__ __forceinline__ void up_item(const TokensArgs& a, const Slots& s, flo
                     g += red[w * 512 + tid];
                     u += red[w * 512 + 256 + tid];
                 }
-                const int i = j * 16 + ((tid >> 2) & 15), r = r0 + t * kRows + (tid >> 6) * 4 + (tid & 3);
-                if (i < n && r < a.I) a.a[(int64_t)s.sorted[first + i] * a.I + r] = (__bf16)(act_value(g, a.act) * u);
+                const int i = j * 16 + ((tid >> 2) & 15), r = t.r0 + k * kRows + (tid >> 6) * 4 + (tid & 3);
+                if (i < t.n && r < a.I) a.a[(int64_t)s.sorted[t.first + i] * a.I + r] = (__bf16)(act_value(g, a.act) * u);
             }
             __syncthreads();
         }
 }
 
+template <class W, int R, int NT>
+__device__ __forceinline__ void up_item(const TokensArgs& a, const Slots& s, float* red, const UpItem& t) {
+    const int lane = threadIdx.x & (kWave - 1), wave = uni(threadIdx.x / kWave);
+    UpShare<W, R, NT> share;
+    f32x4 c[2 * R][NT];
+    share.start(a, s, t, wave, lane);
+    share.run(lane, c);
+    up_finish<R, NT>(a, s, red, t, wave, lane, c);
+}
+
 // MANY: an expert may have more than 16 tokens.  Two tiles of them are the most
 // that the registers hold; a third and fourth are another pass over the weights.
-template <class W, bool MANY, bool ROUTE>
-__global__ void __launch_bounds__(kThreads, 4 / W::kTiles) tokens_up_kernel(TokensArgs a) {
+template <class W, int R, bool MANY, bool ROUTE>
+__global__ void __launch_bounds__(kThreads, W::kUpWaves) tokens_up_kernel(TokensArgs a) {
     __shared__ Slots s;
     __shared__ __attribute__((aligned(16))) float red[kWaves * 512];
     find_slots<ROUTE, kMaxTokens>(a, s);
-    constexpr int kSide = W::kTiles * kRows;
+    constexpr int kSide = R * kRows;
     const int tiles = (a.I + kSide - 1) / kSide, items = uni(s.n_used) * tiles;
     for (int i = blockIdx.x; i < items; i += gridDim.x) {
-        const int u = i / tiles, tile = i - u * tiles;
-        const int e = uni(s.used[u]), first = uni(s.start[u]), n = uni(s.start[u + 1]) - first;
-        if (!MANY || n <= 16) up_item<W, 1>(a, s, red, e, first, n, tile * kSide);
+        const int u = i / tiles, first = uni(s.start[u]);
+        const UpItem t{uni(s.used[u]), first, uni(s.start[u + 1]) - first, (i - u * tiles) * kSide};
+        if (!MANY || t.n <= 16) up_item<W, R, 1>(a, s, red, t);
         else
-            for (int k = 0; k < n; k += 32) up_item<W, 2>(a, s, red, e, first + k, n - k < 32 ? n - k : 32, tile * kSide);
+            for (int k = 0; k < t.n; k += 32) up_item<W, R, 2>(a, s, red, {t.e, first + k, t.n - k < 32 ? t.n - k : 32, t.r0});
     }
 }
 
-// kTiles * 16 columns of y from c0 on.  A wave takes an eighth of the used experts'
+// R row tiles of columns of y from c0 on.  A wave takes an eighth of the used experts'
 // groups, one after another; sums: [wave][token][columns].  An expert's further
 // tokens past 16 read its rows again, out of the L2 where they just were.
-template <class W, int TOKENS>
-__device__ __forceinline__ void down_item(const TokensArgs& a, const Slots& s, float (&sums)[kWaves][TOKENS][W::kTiles * kRows], int c0) {
-    constexpr int D = 4, M = W::kTiles, kSide = M * kRows;
+template <class W, int R, int TOKENS>
+__device__ __forceinline__ void down_item(const TokensArgs& a, const Slots& s, float (&sums)[kWaves][TOKENS][R * kRows], int c0) {
+    constexpr int D = 4, M = R, kSide = M * kRows;
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = uni(tid / kWave), q = lane >> 4;
     const int groups = (a.I + 4 * W::kStep - 1) / (4 * W::kStep), units = uni(s.n_used) * groups;
     const int begin = (int)((int64_t)units * wave / kWaves), end = (int)((int64_t)units * (wave + 1) / kWaves);
@@ -502,20 +538,20 @@ __device__ __forceinline__ void down_item(const TokensArgs& a, const Slots& s, f
     __syncthreads();
 }
 
-// The sums follow the slots: past 64 KiB together with 4-bit weights and many tokens.
-template <class W, int TOKENS>
-constexpr size_t kDownLds = sizeof(Slots) / 16 * 16 + 16 + sizeof(float) * kWaves * TOKENS * W::kTiles * kRows;
+// The sums follow the slots: past 64 KiB together with many tokens.
+template <int R, int TOKENS>
+constexpr size_t kDownLds = sizeof(Slots) / 16 * 16 + 16 + sizeof(float) * kWaves * TOKENS * R * kRows;
 
-template <class W, int TOKENS>
-__global__ void __launch_bounds__(kThreads, 4 / W::kTiles) tokens_down_kernel(TokensArgs a) {
+template <class W, int R, int TOKENS>
+__global__ void __launch_bounds__(kThreads, 4 / R) tokens_down_kernel(TokensArgs a) {
     extern __shared__ __attribute__((aligned(16))) char smem[];
-    constexpr int kSide = W::kTiles * kRows;
+    constexpr int kSide = R * kRows;
     Slots& s = *(Slots*)smem;
     float (&sums)[kWaves][TOKENS][kSide] = *(float (*)[kWaves][TOKENS][kSide])(smem + sizeof(Slots) / 16 * 16 + 16);
     for (int i = threadIdx.x; i < kWaves * TOKENS * kSide; i += kThreads) (&sums[0][0][0])[i] = 0.f;
     find_slots<false, TOKENS == 16 ? kMaxTokens : 16>(a, s);        // of 16 tokens no expert has more
     const int tiles = (a.H + kSide - 1) / kSide;
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) down_item<W, TOKENS>(a, s, sums, tile * kSide);
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) down_item<W, R, TOKENS>(a, s, sums, tile * kSide);
 }
 
 // From so many tokens on, or past 256 experts, the choice has a launch of its own:
@@ -524,27 +560,44 @@ constexpr int kRouteHereTokens = kWaves;
 static_assert(kRouteHereTokens <= 16, "no expert has more");
 constexpr int kRouteHereExperts = 256;
 
-template <class W, bool MANY>
-hipError_t launch(const TokensArgs& a, int num_cu, hipStream_t stream) {
-    constexpr int kSide = W::kTiles * kRows, kTokens = MANY ? kMaxTokens : 16;
-    const int most = 2 / W::kTiles * num_cu;            // what the registers let run at once
-    const int64_t used = (int64_t)a.T * a.K < a.E ? (int64_t)a.T * a.K : a.E;
-    const int64_t up = used * ((a.I + kSide - 1) / kSide), down = (a.H + kSide - 1) / kSide;
-    const int g1 = (int)(up < most ? up : most), g2 = (int)(down < most ? down : most);
+template <class W, int R, bool MANY>
+hipError_t launch_up(const TokensArgs& a, int64_t items, int num_cu, hipStream_t stream) {
+    const int most = W::kUpWaves / 2 * num_cu;          // what the registers let run at once
+    const int grid = (int)(items < most ? items : most);
     bool here = false;
     if constexpr (!MANY) {
         here = a.route_here;
-        if (here) tokens_up_kernel<W, MANY, true><<<g1, kThreads, 0, stream>>>(a);
+        if (here) tokens_up_kernel<W, R, MANY, true><<<grid, kThreads, 0, stream>>>(a);
     }
-    if (!here) tokens_up_kernel<W, MANY, false><<<g1, kThreads, 0, stream>>>(a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    constexpr size_t lds = kDownLds<W, kTokens>;
-    if (lds > 64 * 1024 && (e = hipFuncSetAttribute((const void*)tokens_down_kernel<W, kTokens>, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                                    (int)lds)) != hipSuccess)
-        return e;
-    tokens_down_kernel<W, kTokens><<<g2, kThreads, lds, stream>>>(a);
+    if (!here) tokens_up_kernel<W, R, MANY, false><<<grid, kThreads, 0, stream>>>(a);
     return hipGetLastError();
+}
+
+template <class W, int R, int TOKENS>
+hipError_t launch_down(const TokensArgs& a, int64_t items, int num_cu, hipStream_t stream) {
+    const int most = 2 / R * num_cu, grid = (int)(items < most ? items : most);
+    constexpr size_t lds = kDownLds<R, TOKENS>;
+    if (lds > 64 * 1024) {
+        const hipError_t e = hipFuncSetAttribute((const void*)tokens_down_kernel<W, R, TOKENS>,
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+        if (e != hipSuccess) return e;
+    }
+    tokens_down_kernel<W, R, TOKENS><<<grid, kThreads, lds, stream>>>(a);
+    return hipGetLastError();
+}
+
+// One row tile a wave where two would leave half of the compute units without work.
+template <class W, bool MANY>
+hipError_t launch(const TokensArgs& a, int num_cu, hipStream_t stream) {
+    constexpr int kTokens = MANY ? kMaxTokens : 16;
+    const int64_t used = (int64_t)a.T * a.K < a.E ? (int64_t)a.T * a.K : a.E;
+    auto items = [](int rows, int r) { return (int64_t)((rows + r * kRows - 1) / (r * kRows)); };
+    const bool up_more = used * items(a.I, W::kUpTiles) > num_cu / 2, down_two = items(a.H, 2) > num_cu / 2;
+    const hipError_t e = up_more ? launch_up<W, W::kUpTiles, MANY>(a, used * items(a.I, W::kUpTiles), num_cu, stream)
+                                 : launch_up<W, 1, MANY>(a, used * items(a.I, 1), num_cu, stream);
+    if (e != hipSuccess) return e;
+    return down_two ? launch_down<W, 2, kTokens>(a, items(a.H, 2), num_cu, stream)
+                    : launch_down<W, 1, kTokens>(a, items(a.H, 1), num_cu, stream);
 }
 
 template <class W>
