@@ -74,7 +74,7 @@ struct Shape {
     // kUp: gate columns and then their up columns, in groups of this many
     static constexpr int kPair = 32;
     static constexpr bool kPipelined = PIPELINED;
-    static constexpr bool kAStrided = a_strided(OP), kBStrided = b_strided(OP), kF16 = false, kSwap = false;
+    static constexpr bool kAStrided = a_strided(OP), kBStrided = b_strided(OP), kF16 = false;
     using A = Loader<BM, BK, a_strided(OP), kWaves>;
     using B = Loader<BN, BK, b_strided(OP), kWaves>;
     static constexpr int kLoads = A::kLoads + B::kLoads;

@@ -6,8 +6,7 @@
 // A shape S has the tile's and the waves' sizes BM, BN, WM, WN, the depth BK and
 // number ST of its LDS tiles, kStageBytes of one, the loaders A and B with
 // kLoads of both, kAStrided and kBStrided (whether the operand's summed index is
-// not the contiguous one), kF16 (fp16 values, else bf16) and kSwap (false: a
-// lane's four sums are columns of one row; true: rows of one column).
+// not the contiguous one) and kF16 (fp16 values, else bf16).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -229,8 +228,7 @@ __device__ __forceinline__ void pipelined_tile(typename S::A& la, typename S::B&
         const i32x4 ra = make_rsrc((const void*)(uintptr_t)la.base), rb = make_rsrc((const void*)(uintptr_t)lb.base);
         each<MF * NF>([&](auto product) {
             constexpr int n = product, P = MF * NF, F = MF + NF;
-            if constexpr (S::kSwap) mfma<S::kF16>(acc[n / NF][n % NF], now.a[n / NF], now.b[n % NF]);
-            else mfma<S::kF16>(acc[n / NF][n % NF], now.b[n % NF], now.a[n / NF]);
+            mfma<S::kF16>(acc[n / NF][n % NF], now.b[n % NF], now.a[n / NF]);
             // both end well before the half, so that the last have come when they are needed
             constexpr int R = P * 3 / 4, r0 = n * F / R < F ? n * F / R : F, r1 = (n + 1) * F / R < F ? (n + 1) * F / R : F;
             each<r1 - r0>([&](auto i) {
@@ -308,7 +306,7 @@ __device__ __forceinline__ void plain_tile(typename S::A& la, typename S::B& lb,
             for (int i = 0; i < MF; ++i)
 #pragma unroll
                 for (int j = 0; j < NF; ++j)
-                    acc[i][j] = S::kSwap ? mfma_value<S::kF16>(fa[i], fb[j], acc[i][j]) : mfma_value<S::kF16>(fb[j], fa[i], acc[i][j]);
+                    acc[i][j] = mfma_value<S::kF16>(fb[j], fa[i], acc[i][j]);
         }
     }
     done(acc);

@@ -42,7 +42,7 @@ namespace {
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 // The products: G, P, the next X, and the last X into the results (of tall
-// matrices with the sums of a lane along the other side).
+// matrices through LDS, which turns it).
 enum Op { kGram, kPoly, kNext, kLast, kLastTall };
 constexpr bool is_update(int op) { return op >= kNext; }
 
@@ -56,8 +56,8 @@ constexpr float kGramScale = 1024.0f;
 constexpr float kLow = 2048.0f;             // lo is held at this many times its value
 constexpr int kPartials = 256;              // sums of squares of a matrix at most
 constexpr int kThreads = 256;
-constexpr int kSplit = 64;                  // side of a tile of the split
-constexpr int kSplitTiles = 8;              // tiles of a workgroup
+constexpr int kSplit = 64;                  // side of a tall matrix's tile in the split
+constexpr int kUnit = 512;                  // pieces of 8 values in a unit of the split: such a tile
 
 // `batch` matrices of one shape.  The workspace holds, each for all of them:
 // hi (two, by turns), lo [m, ld_n], g, p [m, ld_m] in fp16, and the partial sums.
@@ -69,11 +69,15 @@ struct Problem {
     char* ws;
     int32_t m, n, ld_m, ld_n;
     int32_t batch;
+    int32_t begin, mats;        // the matrices that a product is for
     int32_t tall;               // x and param are [n, m]
     int32_t partials;           // of a matrix
     float scale;                // the power of two that X is held at
     float step;                 // learning rate times the shape's factor
 
+    // whether pieces of 8 values, of a matrix and of a row of x, start at whole 16 bytes
+    __device__ bool even() const { return ((int64_t)m * n & 7) == 0; }
+    __device__ bool even_rows() const { return ((tall ? m : n) & 7) == 0; }
     __host__ __device__ int64_t x_size() const { return (int64_t)m * ld_n; }
     __host__ __device__ int64_t g_size() const { return (int64_t)m * ld_m; }
     __device__ _Float16* hi(int turn) const { return (_Float16*)ws + turn * batch * x_size(); }
@@ -107,13 +111,69 @@ __device__ __forceinline__ int find_problem(const GroupArgs& a, int i) {
     return __builtin_popcountll(__ballot(lane < a.count && a.first[lane] <= i)) - 1;
 }
 
-__device__ __forceinline__ float load_x(const GroupArgs& a, const void* x, int64_t i) {
-    return a.x_bf16 ? (float)((const __bf16*)x)[i] : ((const float*)x)[i];
+// Eight values, or with even false the first `left` of them and zeros.
+__device__ __forceinline__ void load8(const float* x, int64_t i, bool even, int left, float (&v)[8]) {
+    if (even) {
+        const f32x4 lo = *(const f32x4*)(x + i), hi = *(const f32x4*)(x + i + 4);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            v[q] = lo[q];
+            v[4 + q] = hi[q];
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = q < left ? x[i + q] : 0.0f;
+    }
+}
+__device__ __forceinline__ void load8(const __bf16* x, int64_t i, bool even, int left, float (&v)[8]) {
+    if (even) {
+        const bf16x8 b = *(const bf16x8*)(x + i);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = (float)b[q];
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = q < left ? (float)x[i + q] : 0.0f;
+    }
+}
+__device__ __forceinline__ void load8(bool bf16, const void* x, int64_t i, bool even, int left, float (&v)[8]) {
+    if (bf16) load8((const __bf16*)x, i, even, left, v);
+    else load8((const float*)x, i, even, left, v);
+}
+__device__ __forceinline__ void store8(float* x, int64_t i, bool even, int left, const float (&v)[8]) {
+    if (even) {
+        *(f32x4*)(x + i) = f32x4{v[0], v[1], v[2], v[3]};
+        *(f32x4*)(x + i + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (q < left) x[i + q] = v[q];
+    }
+}
+__device__ __forceinline__ void store8(__bf16* x, int64_t i, bool even, int left, const float (&v)[8]) {
+    if (even) {
+        bf16x8 b;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) b[q] = (__bf16)v[q];
+        *(bf16x8*)(x + i) = b;
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (q < left) x[i + q] = (__bf16)v[q];
+    }
 }
 
 // The update's value from the gradient and the new momentum.
 __device__ __forceinline__ float mix(const GroupArgs& a, float g, float m) {
     return a.nesterov ? a.rest_mu * g + a.mu * m : m;
+}
+
+// Sum over the workgroup, the same in every thread.
+__device__ __forceinline__ double block_sum(double v, double* part) {
+#pragma unroll
+    for (int d = kWave / 2; d >= 1; d >>= 1) v += __shfl_xor(v, d);
+    if ((threadIdx.x & (kWave - 1)) == 0) part[threadIdx.x / kWave] = v;
+    __syncthreads();
+    return (part[0] + part[1]) + (part[2] + part[3]);
 }
 
 // The momentum, and the sums of squares of the update, in double: neither tiny
@@ -123,75 +183,121 @@ __global__ void __launch_bounds__(kThreads) muon_sums_kernel(GroupArgs a) {
     const int i = find_problem(a, blockIdx.x), tid = threadIdx.x;
     const Problem& p = a.p[i];
     const int local = blockIdx.x - a.first[i], mat = local / p.partials, k = local - mat * p.partials;
-    const int64_t n = (int64_t)p.m * p.n, at = mat * n, step = (int64_t)p.partials * kThreads;
+    const int64_t n = (int64_t)p.m * p.n, at = mat * n, step = (int64_t)p.partials * kThreads * 8;
+    const bool even = p.even();
     double sum = 0.0;
-#pragma unroll 4
-    for (int64_t j = (int64_t)k * kThreads + tid; j < n; j += step) {
-        float u = load_x(a, p.x, at + j);
+#pragma unroll 2
+    for (int64_t j = ((int64_t)k * kThreads + tid) * 8; j < n; j += step) {
+        const int left = n - j < 8 ? (int)(n - j) : 8;
+        float u[8];
+        load8(a.x_bf16, p.x, at + j, even, left, u);
         if (p.momentum) {
-            const float m = a.mu * p.momentum[at + j] + a.rest_mu * u;
-            p.momentum[at + j] = m;
-            u = mix(a, u, m);
-        }
-        sum += (double)u * (double)u;
-    }
+            float m[8];
+            load8(p.momentum, at + j, even, left, m);
 #pragma unroll
-    for (int d = kWave / 2; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
-    if ((tid & (kWave - 1)) == 0) part[tid / kWave] = sum;
-    __syncthreads();
-    if (tid == 0) p.sums()[local] = (part[0] + part[1]) + (part[2] + part[3]);
+            for (int q = 0; q < 8; ++q) {
+                m[q] = a.mu * m[q] + a.rest_mu * u[q];
+                u[q] = mix(a, u[q], m[q]);
+            }
+            store8(p.momentum, at + j, even, left, m);
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) sum += (double)u[q] * (double)u[q];
+    }
+    sum = block_sum(sum, part);
+    if (tid == 0) p.sums()[local] = sum;
 }
 
 __device__ __forceinline__ void split(float v, _Float16& hi, _Float16& lo) {
     hi = (_Float16)v;
     lo = (_Float16)((v - (float)hi) * kLow);
 }
+__device__ __forceinline__ void split8(const float (&v)[8], f16x8& hi, f16x8& lo) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        _Float16 h, l;
+        split(v[q], h, l);
+        hi[q] = h;
+        lo[q] = l;
+    }
+}
 
-// X over its norm, as hi and lo, tall matrices transposed; columns past n are zeros.
-__global__ void __launch_bounds__(kThreads) muon_split_kernel(GroupArgs a) {
+// Units of a matrix in the split.
+__host__ __device__ inline int64_t split_units(int m, int ld_n, bool tall) {
+    return tall ? (int64_t)((m + kSplit - 1) / kSplit) * ((ld_n + kSplit - 1) / kSplit) : ((int64_t)m * (ld_n / 8) + kUnit - 1) / kUnit;
+}
+
+// X over its norm, as hi and lo, tall matrices turned through LDS; columns past n
+// are zeros.  per: units of a workgroup.
+__global__ void __launch_bounds__(kThreads) muon_split_kernel(GroupArgs a, int per) {
     __shared__ float tile[kSplit][kSplit + 1];
     __shared__ double part[kThreads / kWave];
     const int i = find_problem(a, blockIdx.x), tid = threadIdx.x;
     const Problem& p = a.p[i];
-    const int down = (p.m + kSplit - 1) / kSplit, across = (p.ld_n + kSplit * kSplitTiles - 1) / (kSplit * kSplitTiles);
-    const int local = blockIdx.x - a.first[i], mat = local / (down * across), t = local - mat * down * across;
+    const int64_t units = split_units(p.m, p.ld_n, p.tall);
+    const int blocks = (int)((units + per - 1) / per), local = blockIdx.x - a.first[i], mat = local / blocks;
     double sum = 0.0;
     for (int k = tid; k < p.partials; k += kThreads) sum += p.sums()[mat * p.partials + k];
-#pragma unroll
-    for (int d = kWave / 2; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
-    if ((tid & (kWave - 1)) == 0) part[tid / kWave] = sum;
-    __syncthreads();
-    const double norm = sqrt((part[0] + part[1]) + (part[2] + part[3]));
+    const double norm = sqrt(block_sum(sum, part));
     const double s = norm == 0.0 ? 0.0 : (double)p.scale / (norm + (double)a.eps);       // a matrix of zeros stays one
     const int64_t at = (int64_t)mat * p.m * p.n;
     _Float16* const hi = p.hi(0) + mat * p.x_size();
     _Float16* const lo = p.lo() + mat * p.x_size();
-    const int r0 = t / across * kSplit;
-    for (int c0 = t % across * kSplitTiles * kSplit, k = 0; k < kSplitTiles && c0 < p.ld_n; ++k, c0 += kSplit) {
-        // in the order of memory: [r][c], tall [c][r]
-        for (int j = tid; j < kSplit * kSplit; j += kThreads) {
-            const int y = j / kSplit, x = j % kSplit;
-            const int r = r0 + (p.tall ? x : y), c = c0 + (p.tall ? y : x);
-            float u = 0.0f;
-            if (r < p.m && c < p.n) {
-                const int64_t from = at + (p.tall ? (int64_t)c * p.m + r : (int64_t)r * p.n + c);
-                u = load_x(a, p.x, from);
-                if (p.momentum) u = mix(a, u, p.momentum[from]);
-            }
-            tile[p.tall ? x : y][p.tall ? y : x] = (float)((double)u * s);
+    const bool even = p.even() && p.even_rows();
+    // a piece of a row of x: pieces past its end are zeros
+    auto load = [&](int64_t from, int left, float (&u)[8]) {
+        if (left <= 0) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) u[q] = 0.0f;
+            return;
+        }
+        load8(a.x_bf16, p.x, from, even, left, u);
+        if (p.momentum) {
+            float m[8];
+            load8(p.momentum, from, even, left, m);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) u[q] = mix(a, u[q], m[q]);
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) u[q] = (float)((double)u[q] * s);
+    };
+    const int64_t first = (int64_t)(local - mat * blocks) * per, last = first + per < units ? first + per : units;
+    if (!p.tall) {
+        const int64_t pieces = (int64_t)p.m * (p.ld_n / 8);
+        const int row = p.ld_n / 8;
+#pragma unroll 2
+        for (int64_t j = first * kUnit + tid; j < last * kUnit && j < pieces; j += kThreads) {
+            const int r = (int)(j / row), c = (int)(j - (int64_t)r * row) * 8;
+            float u[8];
+            load(at + (int64_t)r * p.n + c, p.n - c, u);
+            f16x8 h, l;
+            split8(u, h, l);
+            *(f16x8*)(hi + j * 8) = h;
+            *(f16x8*)(lo + j * 8) = l;
+        }
+        return;
+    }
+    const int across = (p.ld_n + kSplit - 1) / kSplit;
+    for (int64_t t = first; t < last; ++t) {
+        const int r0 = (int)(t / across) * kSplit, c0 = (int)(t % across) * kSplit;
+#pragma unroll
+        for (int k = 0; k < kUnit / kThreads; ++k) {
+            const int j = k * kThreads + tid, y = j / (kSplit / 8), x = j % (kSplit / 8) * 8;
+            float u[8];
+            load(at + (int64_t)(c0 + y) * p.m + r0 + x, c0 + y < p.n ? p.m - r0 - x : 0, u);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) tile[y][x + q] = u[q];
         }
         __syncthreads();
-        for (int j = tid; j < kSplit * kSplit / 8; j += kThreads) {
-            const int y = j / (kSplit / 8), x = j % (kSplit / 8) * 8;
-            if (r0 + y < p.m && c0 + x < p.ld_n) {
-                f16x8 h, l;
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    _Float16 vh, vl;
-                    split(tile[y][x + q], vh, vl);
-                    h[q] = vh;
-                    l[q] = vl;
-                }
+        for (int k = 0; k < kUnit / kThreads; ++k) {
+            const int j = k * kThreads + tid, y = j / (kSplit / 8), x = j % (kSplit / 8) * 8;
+            if (r0 + y < p.m && c0 + x < p.ld_n) {
+                float u[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) u[q] = tile[x + q][y];
+                f16x8 h, l;
+                split8(u, h, l);
                 const int64_t to = (int64_t)(r0 + y) * p.ld_n + c0 + x;
                 *(f16x8*)(hi + to) = h;
                 *(f16x8*)(lo + to) = l;
@@ -209,7 +315,7 @@ struct Shape {
     static constexpr int kThreads = kWaves * kWave;
     static constexpr int kStageBytes = (BM + BN) * BK * 2;
     static constexpr bool kPipelined = PIPELINED;
-    static constexpr bool kAStrided = false, kBStrided = is_update(OP), kF16 = true, kSwap = OP == kLastTall;
+    static constexpr bool kAStrided = false, kBStrided = is_update(OP), kF16 = true;
     using A = Loader<BM, BK, kAStrided, kWaves>;
     using B = Loader<BN, BK, kBStrided, kWaves>;
     static constexpr int kLoads = A::kLoads + B::kLoads;
@@ -235,23 +341,21 @@ __device__ __forceinline__ void eight(const f32x4& v0, const f32x4& v1, float (&
 }
 __device__ __forceinline__ int eight_at(int lane) { return (lane & 16) + (lane >> 5) * 8; }
 
-// Results of consecutive values: bf16, or the parameters' step and their copy.
-__device__ __forceinline__ void write_results(const GroupArgs& a, const Problem& p, int64_t at, int left, const float (&v)[8]) {
+// Eight consecutive results, or `left` of them: bf16, or the parameters' step and
+// their copy.  old: the parameters.
+__device__ __forceinline__ void write_results(const GroupArgs& a, const Problem& p, int64_t at, bool even, int left,
+                                              const float (&old)[8], float (&v)[8]) {
     const float back = 1.0f / p.scale;          // a power of two
-    if (!p.momentum) {
+    if (p.momentum) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-            if (q < left) ((__bf16*)p.param)[at + q] = (__bf16)(v[q] * back);
-        return;
-    }
+        for (int q = 0; q < 8; ++q) v[q] = old[q] * a.decay - p.step * (v[q] * back);
+        if (a.param_bf16) store8((__bf16*)p.param, at, even, left, v);
+        else store8((float*)p.param, at, even, left, v);
+        if (p.copy) store8(p.copy, at, even, left, v);
+    } else {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-        if (q >= left) break;
-        const float old = a.param_bf16 ? (float)((const __bf16*)p.param)[at + q] : ((const float*)p.param)[at + q];
-        const float now = old * a.decay - p.step * (v[q] * back);
-        if (a.param_bf16) ((__bf16*)p.param)[at + q] = (__bf16)now;
-        else ((float*)p.param)[at + q] = now;
-        if (p.copy) p.copy[at + q] = (__bf16)now;
+        for (int q = 0; q < 8; ++q) v[q] *= back;
+        store8((__bf16*)p.param, at, even, left, v);
     }
 }
 
@@ -267,88 +371,123 @@ __device__ __forceinline__ float shift_of(const GroupArgs& a, const Problem& p, 
     return -(a.b * l + a.c * (l * l));
 }
 
-// A wave's part of a finished tile: rows from r_at, columns from c_at; k: the shift.
-template <class S, int MF, int NF>
-__device__ __forceinline__ void finish(const GroupArgs& a, const Problem& p, int mat, int r_at, int c_at, bool mirror, int lane,
-                                       float k, const f32x4 (&acc)[MF][NF]) {
-    constexpr int OP = S::OP;
-    if constexpr (OP == kLastTall) {
-        // lane l holds column l % 16; its rows lie together in the result
-        const _Float16* const hi = p.hi(a.turn) + mat * p.x_size();
-        const _Float16* const lo = p.lo() + mat * p.x_size();
+// Floats of a column of 32 rows in LDS: 4 more spread the columns over the banks.
+constexpr int kTurnRow = 36;
+
+// G's or P's tile and, off the diagonal, its mirror image.
+template <int OP, int MF, int NF>
+__device__ __forceinline__ void finish_square(const GroupArgs& a, const Problem& p, int mat, int r_at, int c_at, bool mirror, int lane,
+                                              float k, const f32x4 (&acc)[MF][NF]) {
+    const _Float16* const g = p.g() + mat * p.g_size();
+    _Float16* const out = (OP == kGram ? p.g() : p.p()) + mat * p.g_size();
 #pragma unroll
-        for (int j = 0; j < NF; ++j) {
-            const int c = c_at + j * 16 + (lane & 15);
+    for (int i = 0; i < MF; ++i) {
+        const int r = r_at + i * 16 + (lane & 15);
+        const bool real = r < p.m;
 #pragma unroll
-            for (int i = 0; i < MF; i += 2) {
-                float v[8];
-                eight(acc[i][j], acc[i + 1][j], v);
-                const int r = r_at + i * 16 + eight_at(lane);
-                if (c >= p.n || r >= p.m) continue;
+        for (int j = 0; j < NF; j += 2) {
+            float v[8];
+            eight(acc[i][j], acc[i][j + 1], v);         // every lane takes part
+            const int c = c_at + j * 16 + eight_at(lane);
+            if (r >= p.ld_m || c >= p.ld_m) continue;
+            f16x8 w;
+            if constexpr (OP == kGram) {
+                const float s = kGramScale / (p.scale * p.scale);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) w[q] = (_Float16)(v[q] * s);
+            } else {
+                f16x8 old = {0, 0, 0, 0, 0, 0, 0, 0};
+                if (real) old = *(const f16x8*)(g + (int64_t)r * p.ld_m + c);
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
-                    if (r + q < p.m) {
-                        const int64_t from = (int64_t)(r + q) * p.ld_n + c;
-                        v[q] = (a.a - k) * ((float)hi[from] + (float)lo[from] * (1.0f / kLow)) + v[q] * (1.0f / kGramScale);
-                    }
-                write_results(a, p, (int64_t)mat * p.m * p.n + (int64_t)c * p.m + r, p.m - r, v);
+                    w[q] = (_Float16)(a.b * (float)old[q] + a.c * (v[q] * (1.0f / kGramScale)) +
+                                      (c + q == r && real ? k * kGramScale : 0.0f));
+            }
+            if (real) *(f16x8*)(out + (int64_t)r * p.ld_m + c) = w;
+            if (mirror)
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    if (c + q < p.m) out[(int64_t)(c + q) * p.ld_m + r] = w[q];
+        }
+    }
+}
+
+// The next X's tile, or the results'; lds: the wave's own part, for tall results.
+template <int OP, int MF, int NF>
+__device__ __forceinline__ void finish_update(const GroupArgs& a, const Problem& p, int mat, int r_at, int c_at, int lane, float k,
+                                              float* lds, const f32x4 (&acc)[MF][NF]) {
+    // Pairs of fragments whose X is loaded together: one by one each would wait
+    // for memory by itself.
+    constexpr int kAcross = NF / 2, kPairs = MF * kAcross, kBatch = 2 * kAcross;
+    static_assert(kPairs % kBatch == 0, "whole batches");
+    const _Float16* const hi = p.hi(a.turn) + mat * p.x_size();
+    _Float16* const lo = p.lo() + mat * p.x_size();
+    const int64_t result = (int64_t)mat * p.m * p.n;
+    const bool even = p.even() && p.even_rows();
+    auto row = [&](int pair) { return r_at + pair / kAcross * 16 + (lane & 15); };
+    auto col = [&](int pair) { return c_at + pair % kAcross * 32 + eight_at(lane); };
+#pragma unroll
+    for (int b = 0; b < kPairs; b += kBatch) {
+        f16x8 h[kBatch], l[kBatch];
+        float old[kBatch][8];
+#pragma unroll
+        for (int t = 0; t < kBatch; ++t) {
+            const int r = row(b + t), c = col(b + t);
+            h[t] = l[t] = f16x8{0, 0, 0, 0, 0, 0, 0, 0};
+            if (r < p.m && c < p.ld_n) {
+                h[t] = *(const f16x8*)(hi + (int64_t)r * p.ld_n + c);
+                l[t] = *(const f16x8*)(lo + (int64_t)r * p.ld_n + c);
+                if (OP == kLast && p.momentum && c < p.n)
+                    load8(a.param_bf16, p.param, result + (int64_t)r * p.n + c, even, p.n - c, old[t]);
             }
         }
-    } else {
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int i = 0; i < MF; ++i) {
-            const int r = r_at + i * 16 + (lane & 15);
+        for (int t = 0; t < kBatch; ++t) {
+            const int pair = b + t, r = row(pair), c = col(pair);
+            float v[8];
+            eight(acc[pair / kAcross][pair % kAcross * 2], acc[pair / kAcross][pair % kAcross * 2 + 1], v);     // every lane
 #pragma unroll
-            for (int j = 0; j < NF; j += 2) {
+            for (int q = 0; q < 8; ++q)
+                v[q] = (a.a - k) * ((float)h[t][q] + (float)l[t][q] * (1.0f / kLow)) + v[q] * (1.0f / kGramScale);
+            if constexpr (OP == kNext) {
+                if (r >= p.m || c >= p.ld_n) continue;
+                f16x8 nh, nl;
+                split8(v, nh, nl);
+                const int64_t at = (int64_t)r * p.ld_n + c;
+                *(f16x8*)(p.hi(a.turn ^ 1) + mat * p.x_size() + at) = nh;
+                *(f16x8*)(lo + at) = nl;
+            } else if constexpr (OP == kLast) {
+                if (r >= p.m || c >= p.n) continue;
+                write_results(a, p, result + (int64_t)r * p.n + c, even, p.n - c, old[t], v);
+            } else {
+                // [column][row]
+                const int y = (pair / kAcross - b / kAcross) * 16 + (lane & 15), x = col(pair) - c_at;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) lds[(x + q) * kTurnRow + y] = v[q];
+            }
+        }
+        if constexpr (OP == kLastTall) {
+            // a wave's LDS accesses keep their order; the fence is for the compiler
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            constexpr int kPieces = 4, kCols = kWave / kPieces;         // of 8 rows
+            const int y = lane % kPieces * 8;
+#pragma unroll
+            for (int x0 = 0; x0 < NF * 16; x0 += kCols) {
+                const int x = x0 + lane / kPieces, r = r_at + b / kAcross * 16 + y, c = c_at + x;
                 float v[8];
-                eight(acc[i][j], acc[i][j + 1], v);         // every lane takes part
-                const int c = c_at + j * 16 + eight_at(lane);
-                if constexpr (OP == kGram || OP == kPoly) {
-                    const _Float16* const g = p.g() + mat * p.g_size();
-                    _Float16* const out = (OP == kGram ? p.g() : p.p()) + mat * p.g_size();
-                    if (r >= p.ld_m || c >= p.ld_m) continue;
-                    const bool real = r < p.m;
-                    f16x8 w;
-                    if constexpr (OP == kGram) {
-                        const float s = kGramScale / (p.scale * p.scale);
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) w[q] = (_Float16)(v[q] * s);
-                    } else {
-                        f16x8 old = {0, 0, 0, 0, 0, 0, 0, 0};
-                        if (real) old = *(const f16x8*)(g + (int64_t)r * p.ld_m + c);
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            w[q] = (_Float16)(a.b * (float)old[q] + a.c * (v[q] * (1.0f / kGramScale)) +
-                                              (c + q == r && real ? k * kGramScale : 0.0f));
-                    }
-                    if (real) *(f16x8*)(out + (int64_t)r * p.ld_m + c) = w;
-                    if (mirror)
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            if (c + q < p.m) out[(int64_t)(c + q) * p.ld_m + r] = w[q];
-                } else {
-                    if (r >= p.m || c >= p.ld_n) continue;
-                    const int64_t at = mat * p.x_size() + (int64_t)r * p.ld_n + c;
-                    const f16x8 h = *(const f16x8*)(p.hi(a.turn) + at), l = *(const f16x8*)(p.lo() + at);
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        v[q] = (a.a - k) * ((float)h[q] + (float)l[q] * (1.0f / kLow)) + v[q] * (1.0f / kGramScale);
-                    if constexpr (OP == kNext) {
-                        f16x8 nh, nl;
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            _Float16 vh, vl;
-                            split(v[q], vh, vl);
-                            nh[q] = vh;
-                            nl[q] = vl;
-                        }
-                        *(f16x8*)(p.hi(a.turn ^ 1) + at) = nh;
-                        *(f16x8*)(p.lo() + at) = nl;
-                    } else {
-                        write_results(a, p, (int64_t)mat * p.m * p.n + (int64_t)r * p.n + c, p.n - c, v);
-                    }
+                *(f32x4*)v = *(const f32x4*)(lds + x * kTurnRow + y);
+                *(f32x4*)(v + 4) = *(const f32x4*)(lds + x * kTurnRow + y + 4);
+                if (r < p.m && c < p.n) {
+                    const int64_t at = result + (int64_t)c * p.m + r;
+                    float before[8] = {};
+                    if (p.momentum) load8(a.param_bf16, p.param, at, even, p.m - r, before);
+                    write_results(a, p, at, even, p.m - r, before, v);
                 }
             }
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         }
     }
 }
@@ -367,7 +506,7 @@ __global__ void __launch_bounds__(S::kThreads) muon_gemm_kernel(GroupArgs a) {
         const int i = uni(find_problem(a, t));
         const Problem& p = a.p[i];
         const int per = (int)tiles_of<BM, BN>(OP, p.m, p.ld_n), local = t - a.first[i];
-        const int mat = local / per, in = local - mat * per;
+        const int mat = p.begin + local / per, in = local % per;
         int mt, nt;
         if constexpr (is_update(OP)) {
             const int tiles_m = (p.m + BM - 1) / BM, tiles_n = (p.ld_n + BN - 1) / BN;
@@ -411,7 +550,19 @@ __global__ void __launch_bounds__(S::kThreads) muon_gemm_kernel(GroupArgs a) {
                 k = OP == kPoly ? shift_of(a, p, mat, lane) : p.shift(mat);
                 if (OP == kPoly && in == 0 && tid == 0) p.shift(mat) = k;
             }
-            finish<S, WM / 16, WN / 16>(a, p, mat, m0 + r, n0 + c, mt != nt, lane, k, acc);
+            if constexpr (is_update(OP)) {
+                float* own = nullptr;
+                if constexpr (OP == kLastTall) {
+                    // the tiles in LDS are done with, and zeros past the last one have arrived
+                    wait_loads<0>();
+                    __builtin_amdgcn_s_barrier();
+                    static_assert(sizeof(float) * WN * kTurnRow <= S::kLds / S::kWaves, "LDS of a wave");
+                    own = (float*)smem + wave * (int)(S::kLds / S::kWaves / sizeof(float));
+                }
+                finish_update<OP, WM / 16, WN / 16>(a, p, mat, m0 + r, n0 + c, lane, k, own, acc);
+            } else {
+                finish_square<OP, WM / 16, WN / 16>(a, p, mat, m0 + r, n0 + c, mt != nt, lane, k, acc);
+            }
         };
         if constexpr (S::kPipelined) pipelined_tile<S, WM / 16, WN / 16>(la, lb, K, r, c, wave, lane, lds, done);
         else plain_tile<S>(la, lb, K, r, c, wave, lane, lds, done);
@@ -429,7 +580,7 @@ int64_t set_tiles(GroupArgs& a) {
     int64_t total = 0;
     for (int i = 0; i < a.count; ++i) {
         a.first[i] = (int32_t)total;
-        total += a.p[i].batch * tiles_of<S::BM, S::BN>(S::OP, a.p[i].m, a.p[i].ld_n);
+        total += a.p[i].mats * tiles_of<S::BM, S::BN>(S::OP, a.p[i].m, a.p[i].ld_n);
     }
     a.first[a.count] = (int32_t)total;
     return total;
@@ -471,13 +622,18 @@ hipError_t run_group(GroupArgs& a, int steps, int num_cu, hipStream_t stream) {
     muon_sums_kernel<<<(int)blocks, kThreads, 0, stream>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    blocks = 0;
-    for (int i = 0; i < a.count; ++i) {
-        a.first[i] = (int32_t)blocks;
-        const Problem& p = a.p[i];
-        blocks += (int64_t)p.batch * ((p.m + kSplit - 1) / kSplit) * ((p.ld_n + kSplit * kSplitTiles - 1) / (kSplit * kSplitTiles));
+    // fewer units a workgroup where there are few
+    int per = 8;
+    for (;; per /= 4) {
+        blocks = 0;
+        for (int i = 0; i < a.count; ++i) {
+            a.first[i] = (int32_t)blocks;
+            const Problem& p = a.p[i];
+            blocks += (int64_t)p.batch * ((split_units(p.m, p.ld_n, p.tall) + per - 1) / per);
+        }
+        if (per < 4 || blocks >= 4 * num_cu) break;
     }
-    muon_split_kernel<<<(int)blocks, kThreads, 0, stream>>>(a);
+    muon_split_kernel<<<(int)blocks, kThreads, 0, stream>>>(a, per);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     for (int s = 0; s < steps; ++s) {
         a.shifted = s + 2 >= steps;
@@ -566,7 +722,8 @@ struct Runner {
             }
             const int64_t k = batch - done < fit ? batch - done : fit;
             Problem& q = a.p[a.count++] = p;
-            q.batch = (int32_t)k;
+            q.batch = q.mats = (int32_t)k;
+            q.begin = 0;
             q.x = (const char*)p.x + done * n * x_size;
             if (p.momentum) q.momentum = p.momentum + done * n;
             q.param = (char*)p.param + done * n * param_size;
