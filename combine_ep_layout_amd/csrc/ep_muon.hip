@@ -29,6 +29,7 @@
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
+#include <atomic>
 #include <new>
 #include <vector>
 
@@ -570,7 +571,6 @@ __global__ void __launch_bounds__(S::kThreads) muon_gemm_kernel(GroupArgs a) {
     wait_loads<0>();        // no load into LDS outlives the workgroup
 }
 
-// Wide tiles when they fill the compute units, lower ones when they do not.
 template <int OP> using Wide = Shape<OP, 256, 256, 128, 64, 2, true>;
 template <int OP> using Middle = Shape<OP, 128, 128, 64, 64, 2, false>;
 template <int OP> using Small = Shape<OP, 64, 64, 32, 32, 4, false>;
@@ -586,40 +586,94 @@ int64_t set_tiles(GroupArgs& a) {
     return total;
 }
 
+// Where a call runs.
+struct Place {
+    int device, num_cu;
+    hipStream_t stream;
+};
+
 template <class S>
-hipError_t launch_shape(GroupArgs& a, int num_cu, hipStream_t stream) {
-    const int64_t tiles = set_tiles<S>(a), most = (int64_t)num_cu * (int64_t)(kLdsBytes / S::kLds);
-    hipError_t e = hipFuncSetAttribute((const void*)muon_gemm_kernel<S>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)S::kLds);
-    if (e != hipSuccess) return e;
-    muon_gemm_kernel<S><<<(int)(tiles < most ? tiles : most), S::kThreads, S::kLds, stream>>>(a);
+hipError_t launch_shape(GroupArgs& a, const Place& at) {
+    const int64_t tiles = set_tiles<S>(a), most = (int64_t)at.num_cu * (int64_t)(kLdsBytes / S::kLds);
+    if (tiles == 0) return hipSuccess;
+    static std::atomic<uint64_t> allowed{0};            // devices that know of the LDS
+    const uint64_t bit = at.device < 64 ? (uint64_t)1 << at.device : 0;
+    if (!(allowed.load(std::memory_order_relaxed) & bit)) {
+        const hipError_t e = hipFuncSetAttribute((const void*)muon_gemm_kernel<S>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)S::kLds);
+        if (e != hipSuccess) return e;
+        allowed.fetch_or(bit, std::memory_order_relaxed);
+    }
+    muon_gemm_kernel<S><<<(int)(tiles < most ? tiles : most), S::kThreads, S::kLds, at.stream>>>(a);
     return hipGetLastError();
 }
 
+// Rounds of wide tiles that so many middle ones cost, two on a compute unit (8
+// matrices of 2048 x 7168, G: 183 us a wide round, 119 one of 512 middle tiles).
+double middle_cost(int64_t tiles, int num_cu) {
+    const int64_t rest = tiles % (2 * num_cu);
+    return 0.65 * (double)(tiles / (2 * num_cu)) + (rest == 0 ? 0.0 : rest <= num_cu ? 0.42 : 0.65);
+}
+
+// The tiles of a product.  Wide ones are the fastest where they come in whole
+// rounds of the compute units; what is left of a last round goes to the middle
+// ones, by whole matrices (8 matrices, G: 252 wide and 136 middle tiles instead of
+// two rounds of 288).  Less than 5/8 of a compute unit's worth of middle tiles:
+// small ones (16 matrices of 256 x 512, the next X: 8.4 us, 13.0).
 template <int OP>
-hipError_t launch_product(GroupArgs& a, int num_cu, hipStream_t stream) {
-    if (set_tiles<Wide<OP>>(a) >= num_cu) return launch_shape<Wide<OP>>(a, num_cu, stream);
-    if (set_tiles<Middle<OP>>(a) >= num_cu) return launch_shape<Middle<OP>>(a, num_cu, stream);
-    return launch_shape<Small<OP>>(a, num_cu, stream);
+hipError_t launch_product(GroupArgs& a, const Place& at) {
+    const int64_t wide = set_tiles<Wide<OP>>(a), middle = set_tiles<Middle<OP>>(a), cu = at.num_cu;
+    if (middle < cu * 5 / 8) return launch_shape<Small<OP>>(a, at);
+    const double all_wide = (double)((wide + cu - 1) / cu), all_middle = middle_cost(middle, (int)cu);
+    GroupArgs rest = a;
+    double best = all_wide < all_middle ? all_wide : all_middle;
+    bool mixed = false;
+    if (wide > cu && wide % cu != 0) {
+        // the fewest matrices from the end on that leave whole rounds
+        GroupArgs front = a;
+        rest.count = 0;
+        int64_t over = wide % cu, less = 0, more = 0;
+        for (int i = a.count - 1; i >= 0 && less < over; --i) {
+            const Problem& p = a.p[i];
+            const int64_t each = tiles_of<256, 256>(OP, p.m, p.ld_n);
+            int64_t k = (over - less + each - 1) / each;
+            k = k < p.mats ? k : p.mats;
+            Problem& q = rest.p[rest.count++] = p;
+            q.begin = p.begin + p.mats - (int)k;
+            q.mats = (int)k;
+            front.p[i].mats = p.mats - (int)k;
+            if (front.p[i].mats == 0) front.count = i;
+            less += k * each;
+            more += k * tiles_of<128, 128>(OP, p.m, p.ld_n);
+        }
+        const double cost = (double)((wide - less + cu - 1) / cu) + middle_cost(more, (int)cu);
+        if (front.count > 0 && cost < best - 0.05) {            // another launch costs something, too
+            mixed = true;
+            const hipError_t e = launch_shape<Wide<OP>>(front, at);
+            if (e != hipSuccess) return e;
+        }
+    }
+    if (mixed) return launch_shape<Middle<OP>>(rest, at);
+    return all_wide < all_middle ? launch_shape<Wide<OP>>(a, at) : launch_shape<Middle<OP>>(a, at);
 }
 
 // The last products of the wide or of the tall problems.
 template <int OP>
-hipError_t launch_last(const GroupArgs& a, int num_cu, hipStream_t stream) {
+hipError_t launch_last(const GroupArgs& a, const Place& at) {
     GroupArgs some = a;
     some.count = 0;
     for (int i = 0; i < a.count; ++i)
         if (a.p[i].tall == (OP == kLastTall)) some.p[some.count++] = a.p[i];
-    return some.count ? launch_product<OP>(some, num_cu, stream) : hipSuccess;
+    return some.count ? launch_product<OP>(some, at) : hipSuccess;
 }
 
-hipError_t run_group(GroupArgs& a, int steps, int num_cu, hipStream_t stream) {
+hipError_t run_group(GroupArgs& a, int steps, const Place& at) {
     int64_t blocks = 0;
     for (int i = 0; i < a.count; ++i) {
         a.first[i] = (int32_t)blocks;
         blocks += (int64_t)a.p[i].batch * a.p[i].partials;
     }
     a.turn = 0;
-    muon_sums_kernel<<<(int)blocks, kThreads, 0, stream>>>(a);
+    muon_sums_kernel<<<(int)blocks, kThreads, 0, at.stream>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     // fewer units a workgroup where there are few
@@ -631,16 +685,16 @@ hipError_t run_group(GroupArgs& a, int steps, int num_cu, hipStream_t stream) {
             const Problem& p = a.p[i];
             blocks += (int64_t)p.batch * ((split_units(p.m, p.ld_n, p.tall) + per - 1) / per);
         }
-        if (per < 4 || blocks >= 4 * num_cu) break;
+        if (per < 4 || blocks >= 4 * at.num_cu) break;
     }
-    muon_split_kernel<<<(int)blocks, kThreads, 0, stream>>>(a, per);
+    muon_split_kernel<<<(int)blocks, kThreads, 0, at.stream>>>(a, per);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     for (int s = 0; s < steps; ++s) {
         a.shifted = s + 2 >= steps;
-        if ((e = launch_product<kGram>(a, num_cu, stream)) != hipSuccess) return e;
-        if ((e = launch_product<kPoly>(a, num_cu, stream)) != hipSuccess) return e;
-        if (s + 1 < steps) e = launch_product<kNext>(a, num_cu, stream);
-        else if ((e = launch_last<kLast>(a, num_cu, stream)) == hipSuccess) e = launch_last<kLastTall>(a, num_cu, stream);
+        if ((e = launch_product<kGram>(a, at)) != hipSuccess) return e;
+        if ((e = launch_product<kPoly>(a, at)) != hipSuccess) return e;
+        if (s + 1 < steps) e = launch_product<kNext>(a, at);
+        else if ((e = launch_last<kLast>(a, at)) == hipSuccess) e = launch_last<kLastTall>(a, at);
         if (e != hipSuccess) return e;
         a.turn ^= 1;
     }
@@ -697,11 +751,11 @@ struct Runner {
     char* ws;
     int64_t bytes, used = 0;
     int64_t tiles = 0;
-    int steps, num_cu;
-    hipStream_t stream;
+    int steps;
+    Place at;
 
     hipError_t flush() {
-        hipError_t e = a.count ? run_group(a, steps, num_cu, stream) : hipSuccess;
+        hipError_t e = a.count ? run_group(a, steps, at) : hipSuccess;
         a.count = 0;
         used = tiles = 0;
         return e;
@@ -737,10 +791,9 @@ struct Runner {
     }
 };
 
-bool cu_count(int& n) {
-    int device = 0;
-    return hipGetDevice(&device) == hipSuccess &&
-           hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, device) == hipSuccess && n > 0;
+bool here(Place& at) {
+    return hipGetDevice(&at.device) == hipSuccess &&
+           hipDeviceGetAttribute(&at.num_cu, hipDeviceAttributeMultiprocessorCount, at.device) == hipSuccess && at.num_cu > 0;
 }
 
 bool fine(const double (&c)[3]) { return std::isfinite(c[0]) && std::isfinite(c[1]) && std::isfinite(c[2]); }
@@ -791,8 +844,8 @@ ep_status ep_orthogonalize(const void* x, int64_t batch, int32_t rows, int32_t c
     run.ws = (char*)workspace;
     run.bytes = workspace_bytes;
     run.steps = steps;
-    run.stream = stream;
-    if (!cu_count(run.num_cu)) return EP_ERR_HIP;
+    run.at.stream = stream;
+    if (!here(run.at)) return EP_ERR_HIP;
     run.a.x_bf16 = bf16;
     run.a.a = (float)k[0];
     run.a.b = (float)k[1];
@@ -853,8 +906,8 @@ ep_status ep_muon(const ep_muon_tensor* tensors, int32_t count, const ep_muon_co
     run.ws = (char*)workspace;
     run.bytes = workspace_bytes;
     run.steps = cfg->steps;
-    run.stream = stream;
-    if (!cu_count(run.num_cu)) return EP_ERR_HIP;
+    run.at.stream = stream;
+    if (!here(run.at)) return EP_ERR_HIP;
     GroupArgs& a = run.a;
     a.x_bf16 = gb;
     a.param_bf16 = pb;
