@@ -11,9 +11,9 @@
 // eight waves, so that all of the chip's compute units read at once however few
 // the experts are.  A wave's product is a matrix instruction with 16 rows of
 // the weights on one side and up to 16 tokens of the expert on the other: the
-// weights go from memory to the registers in the instruction's own layout,
-// several steps ahead, with no pass through LDS, and further tokens of the same
-// expert cost no bytes.  The waves' sums meet in LDS, in a fixed order.
+// weights go from memory to the registers in the instruction's own layout, a step
+// ahead, with no pass through LDS, and further tokens of the same expert cost no
+// bytes of theirs.  The waves' sums meet in LDS, in a fixed order.
 //
 // Weights are bf16, or 4-bit codes (e2m1) with an exponent byte for each 32 of
 // them: two codes become two bf16 values, exactly, in one instruction, so the
@@ -80,7 +80,7 @@ __device__ __forceinline__ u32x4 load16(Buffer b, uint32_t lane, int at) {
 // quarter q = l / 16 in kFrags fragments of 8.
 // kUpTiles: row tiles of a wave in the gate and up products.  Two share what is
 // loaded of the tokens, which beside 4-bit weights is as many bytes as the
-// weights (64 tokens: 278 us, 338 with one); beside bf16 weights it is little, and
+// weights (64 tokens: 267 us, 338 with one); beside bf16 weights it is little, and
 // two workgroups of a compute unit that hide each other's ends are worth more
 // (24 experts of 2056 x 1000: 38 us, 43).  kUpWaves: waves of a SIMD so.
 struct Bf16Weights {
@@ -192,8 +192,13 @@ __device__ __forceinline__ void find_slots(const TokensArgs& a, Slots& s) {
         if (wave < a.T) {
             int mine;
             float weight;
-            if (a.route.bias) route_token<4, true>(a.route, wave, lane, mine, weight);
-            else route_token<4, false>(a.route, wave, lane, mine, weight);
+            if (a.E <= kWave) {
+                if (a.route.bias) route_token<1, true>(a.route, wave, lane, mine, weight);
+                else route_token<1, false>(a.route, wave, lane, mine, weight);
+            } else {
+                if (a.route.bias) route_token<4, true>(a.route, wave, lane, mine, weight);
+                else route_token<4, false>(a.route, wave, lane, mine, weight);
+            }
             if (lane < a.K) {
                 const int at = wave * a.K + lane;
                 s.expert[at] = (int16_t)mine;
@@ -212,6 +217,33 @@ __device__ __forceinline__ void find_slots(const TokensArgs& a, Slots& s) {
         }
     }
     __syncthreads();
+    if (a.T == 1) {             // the slots themselves, by one wave
+        if (wave == 0) {
+            const int e = lane < a.K ? s.expert[lane] : -1;
+            float w = lane < a.K ? s.weight[lane] : 0.0f;
+            bool first = e >= 0;
+            for (int j = 0; j < a.K; ++j) {
+                const int other = __builtin_amdgcn_readlane(e, j);
+                const float more = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(w), j));
+                if (other == e && j < lane) first = false;
+                if (other == e && j > lane) w += more;          // this lane's own sum, of slots that are no first ones
+            }
+            const uint64_t who = __ballot(first);
+            const int u = __builtin_popcountll(who & ((1ull << lane) - 1)), n = __builtin_popcountll(who);
+            if (first) {
+                s.used[u] = (int16_t)e;
+                s.start[u] = u;
+                s.sorted[u] = (int16_t)lane;
+                s.weight[lane] = w;
+            }
+            if (lane == 0) {
+                s.n_used = n;
+                s.start[n] = n;
+            }
+        }
+        __syncthreads();
+        return;
+    }
     // An expert that a token names twice is one product with both weights.
     for (int i = tid; i < S; i += kThreads) {
         const int e = s.expert[i], t = i / a.K, end = (t + 1) * a.K;
@@ -285,18 +317,19 @@ struct Stage {
     u32x4 x[NT][W::kFrags];
 };
 
-// A wave's stream of steps, D of them loaded ahead and the group's scales one
-// group ahead.  S says what a step is: the matrices and lanes, and the tokens' rows.
-template <class W, int M, int NT, int D>
+// A wave's stream of steps: the next one's loads follow each step's products, a
+// group's scales are loaded a group ahead.  One step ahead keeps enough bytes on
+// their way (16 waves of 4 KiB a compute unit); more of them cost (one token in
+// bf16: 131 us, 142 with four steps; 64 tokens in 4 bits: 426 us, 444).
+template <class W, int M, int NT>
 struct Stream {
-    static_assert(4 % D == 0, "a group is four steps");
-    Stage<W, M, NT> stage[D];
+    Stage<W, M, NT> stage;
     typename W::Scales scales[M], ahead[M];
 
     // x_at: the lane's token's offset in bytes, or kOutOfRange.  left <= 0: nothing (every lane out of range).
-    __device__ __forceinline__ void load(int d, const typename W::Matrix (&m)[M], const typename W::Lane (&l)[M], Buffer x,
+    __device__ __forceinline__ void load(const typename W::Matrix (&m)[M], const typename W::Lane (&l)[M], Buffer x,
                                          const uint32_t (&x_at)[NT], int step, int left, int q) {
-        Stage<W, M, NT>& s = stage[d % D];
+        Stage<W, M, NT>& s = stage;
         // The buffers' range is checked less the common offset, which therefore stays inside.
         step = left > 0 ? step : 0;
 #pragma unroll
@@ -306,7 +339,7 @@ struct Stream {
 #pragma unroll
             for (int f = 0; f < W::kFrags; ++f)
                 s.x[j][f] = load16(x, W::k_of(q, f) < left ? x_at[j] + W::k_of(q, f) * 2 : kOutOfRange, step * (W::kStep * 2));
-        __builtin_amdgcn_sched_barrier(0);      // in this order, or the first wait in a loop would be for all of them
+        __builtin_amdgcn_sched_barrier(0);
     }
     __device__ __forceinline__ void load_scales(const typename W::Matrix (&m)[M], const typename W::Lane (&l)[M], int step, int n) {
 #pragma unroll
@@ -321,7 +354,7 @@ struct Stream {
         }
     }
     __device__ __forceinline__ void multiply(int d, const typename W::Lane (&l)[M], int left, int q, f32x4 (&c)[M][NT]) const {
-        const Stage<W, M, NT>& s = stage[d % D];
+        const Stage<W, M, NT>& s = stage;
         float scale[M];
 #pragma unroll
         for (int i = 0; i < M; ++i) scale[i] = W::scale_of(scales[i], l[i], d, left, q);
@@ -345,13 +378,13 @@ struct UpItem {
 // A wave's share of an item: an eighth of the summed index.
 template <class W, int R, int NT>
 struct UpShare {
-    static constexpr int D = NT == 1 ? 4 : 2, M = 2 * R;
+    static constexpr int M = 2 * R;
     typename W::Matrix m[M];
     typename W::Lane l[M];
     uint32_t x_at[NT];
     Buffer x;
     int begin, end, H;
-    Stream<W, M, NT, D> stream;
+    Stream<W, M, NT> stream;
 
     __device__ __forceinline__ int left(int i) const { return i < end ? H - i * W::kStep : 0; }
 
@@ -377,8 +410,7 @@ struct UpShare {
         end = steps * (wave + 1) / kWaves;
         if (begin == end) return;
         stream.load_scales(m, l, begin, H);
-#pragma unroll
-        for (int d = 0; d < D; ++d) stream.load(d, m, l, x, x_at, begin + d, left(begin + d), q);
+        stream.load(m, l, x, x_at, begin, left(begin), q);
     }
     __device__ __forceinline__ void run(int lane, f32x4 (&c)[M][NT]) {
         const int q = lane >> 4;
@@ -393,7 +425,7 @@ struct UpShare {
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
                 stream.multiply(d, l, left(i + d), q, c);
-                stream.load(d, m, l, x, x_at, i + d + D, left(i + d + D), q);
+                stream.load(m, l, x, x_at, i + d + 1, left(i + d + 1), q);
             }
         }
     }
@@ -461,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, W::kUpWaves) tokens_up_kernel(Tokens
 // tokens past 16 read its rows again, out of the L2 where they just were.
 template <class W, int R, int TOKENS>
 __device__ __forceinline__ void down_item(const TokensArgs& a, const Slots& s, float (&sums)[kWaves][TOKENS][R * kRows], int c0) {
-    constexpr int D = 4, M = R, kSide = M * kRows;
+    constexpr int M = R, kSide = M * kRows;
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = uni(tid / kWave), q = lane >> 4;
     const int groups = (a.I + 4 * W::kStep - 1) / (4 * W::kStep), units = uni(s.n_used) * groups;
     const int begin = (int)((int64_t)units * wave / kWaves), end = (int)((int64_t)units * (wave + 1) / kWaves);
@@ -469,7 +501,7 @@ __device__ __forceinline__ void down_item(const TokensArgs& a, const Slots& s, f
 #pragma unroll
     for (int i = 0; i < M; ++i) l[i] = W::lane(c0 + i * kRows + (lane & 15), a.H, a.I, q);
     const Buffer x = buffer(a.a, (int64_t)a.T * a.K * a.I * 2);
-    Stream<W, M, 1, D> stream;
+    Stream<W, M, 1> stream;
     f32x4 c[M][1];
 #pragma unroll
     for (int i = 0; i < M; ++i) c[i][0] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -487,20 +519,23 @@ __device__ __forceinline__ void down_item(const TokensArgs& a, const Slots& s, f
         int u = begin / groups, g = begin - u * groups;         // where the products are
         open(u);
         stream.load_scales(m, l, g * 4, a.I);
-#pragma unroll
-        for (int d = 0; d < 4; ++d) stream.load(d, m, l, x, x_at, g * 4 + d, a.I - (g * 4 + d) * W::kStep, q);
+        stream.load(m, l, x, x_at, g * 4, a.I - g * 4 * W::kStep, q);
 #pragma unroll 1
         for (int i = begin; i < end; ++i) {
             // the next group: of this expert, or of the next one
             const bool more = i + 1 < end;
             const int next_g = g + 1 == groups ? 0 : g + 1;
-            if (more && next_g == 0) open(u + 1);
             stream.next_group();
-            stream.load_scales(m, l, more ? next_g * 4 : 0, a.I);
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
                 stream.multiply(d, l, a.I - (g * 4 + d) * W::kStep, q, c);
-                stream.load(d, m, l, x, x_at, next_g * 4 + d, more ? a.I - (next_g * 4 + d) * W::kStep : 0, q);
+                if (d < 3) {
+                    stream.load(m, l, x, x_at, g * 4 + d + 1, a.I - (g * 4 + d + 1) * W::kStep, q);
+                } else {
+                    if (more && next_g == 0) open(u + 1);
+                    stream.load_scales(m, l, more ? next_g * 4 : 0, a.I);
+                    stream.load(m, l, x, x_at, next_g * 4, more ? a.I - next_g * 4 * W::kStep : 0, q);
+                }
             }
             if (next_g == 0 || !more) {
                 // the expert's part is done: every token has it once
