@@ -670,6 +670,7 @@ extern "C" ep_status ep_moe_tokens(const ep_moe_tokens_args* p, hipStream_t stre
     if (!p->x || !p->topk_idx || !p->topk_weights || !p->w_gate_up || !p->w_down || !p->act || !p->y || !aligned(p->x, 16) ||
         !aligned(p->topk_idx, 4) || !aligned(p->topk_weights, 4) || !aligned(p->bias, 4) || !aligned(p->w_gate_up, 16) ||
         !aligned(p->w_down, 16) || !aligned(p->act, 16) || !aligned(p->y, 16) ||
+        !aligned(p->gate_up_scales, 16) || !aligned(p->down_scales, 16) ||
         four != (p->gate_up_scales != nullptr) || four != (p->down_scales != nullptr))
         return EP_ERR_INVALID_ARGUMENT;
     // nothing that is written shares memory with anything else

@@ -472,7 +472,7 @@ ep_status ep_expert_ffn_backward(const ep_handle* h, uint32_t epoch, const void*
  *   y               device bf16 [num_tokens, hidden]; a token without an expert
  *                   gets zeros.
  * Pointers are 16-byte aligned; logits, bias, topk_idx and topk_weights as
- * ep_route wants them, scale bytes anyhow.  Nothing that is written shares
+ * ep_route wants them.  Nothing that is written shares
  * memory with anything else (EP_ERR_INVALID_ARGUMENT).  Sums are fp32 in a fixed
  * order, weights included; a and y are each rounded once.  A token's row of y
  * depends on nothing of the other tokens but the order of its sums: infinities

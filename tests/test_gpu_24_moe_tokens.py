@@ -144,6 +144,31 @@ def test_an_expert_named_twice(four):
     check_y(y, x, idx, w, up, down, "silu")
 
 
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("K", [1, 2, 7, 32])
+def test_one_token_names_experts_twice_and_none(K, four):
+    """One token's slots are found by one wave: repeats, masked slots, all of them one expert, all masked."""
+    import combine_ep_layout_amd as ep
+    q, (up, down) = weights(9, 96, 160, four, K)
+    x = rows(1, 96, K)
+    g = torch.Generator(device=dev()).manual_seed(K)
+    w = torch.randn(1, K, device=dev(), generator=g)
+    ids = torch.randint(-2, 11, (1, K), device=dev(), generator=g).to(torch.int32)       # 9 and 10 are no experts
+    for idx in (ids, torch.full_like(ids, 8), torch.full_like(ids, -1)):
+        y = ep.moe_tokens(x, *q, topk_idx=idx, topk_weights=w)[0]
+        check_y(y, x, idx, w, up, down, "silu")
+    assert not y.any()
+
+
+def test_a_part_of_the_experts():
+    """Slices of the experts' matrices are matrices as well."""
+    import combine_ep_layout_amd as ep
+    q, (up, down) = weights(7, 160, 96, True, 9)
+    part = [ep.Mxfp4(w.codes[3:6], w.scales[3:6]) for w in q]
+    x, (idx, w) = rows(5, 160, 9), routing(5, 3, 2, 9)
+    check_y(ep.moe_tokens(x, *part, topk_idx=idx, topk_weights=w)[0], x, idx, w, up[3:6], down[3:6], "silu")
+
+
 def test_rows_of_nan_and_infinity_stay_apart():
     """Padding rows of a batch may hold anything; strided rows leave what lies between them out."""
     import combine_ep_layout_amd as ep

@@ -97,6 +97,28 @@ def test_workspace_of_one_matrix(shape):
         ep.orthogonalize(x, workspace=room[:one // 16 * 16 - 16])
 
 
+@pytest.mark.parametrize("shape", [(90, 768, 800), (90, 800, 768)], ids=str)
+def test_whole_rounds_and_a_rest(shape):
+    """Batches whose products go to wide tiles in whole rounds of 256 compute units and to middle ones for the rest."""
+    import combine_ep_layout_amd as ep
+    x = ref.matrices("noise", *shape, dev(), 11).bfloat16()
+    out = ep.orthogonalize(x)
+    ref.check("X", out, x)
+    assert torch.equal(ep.orthogonalize(x), out)
+    ref.near(in_fp32(x, 2), x, 2)
+
+
+def test_a_rest_of_two_tensors():
+    """The rest of the wide tiles' rounds takes one tensor whole and the last matrix of another."""
+    import combine_ep_layout_amd as ep
+    shapes = [(86, 768, 800), (2, 530, 520)]
+    x = [ref.matrices("noise", *s, dev(), s[1]).bfloat16() for s in shapes]
+    p, m = ([torch.zeros(s, device=dev()) for s in shapes] for _ in range(2))
+    ep.muon(p, x, m, lr=-1.0, momentum=0.0, weight_decay=0.0, nesterov=False, scale=1.0, steps=2)
+    for got, u in zip(p, x):
+        ref.near(got, u, 2)
+
+
 def step_inputs(shapes, p_dtype, g_dtype, copy, seed):
     g = torch.Generator(device=dev()).manual_seed(seed)
     n = lambda s, std: torch.randn(s, device=dev(), generator=g) * std

@@ -51,6 +51,7 @@ def test_moe_tokens_refusals(ep):
                 dict(logits=None, bias=A[8]), dict(logits=A[1] + 2), dict(x=None), dict(x=A[0] + 8), dict(topk_idx=None),
                 dict(topk_weights=None), dict(topk_idx=A[2] + 2), dict(w_gate_up=None), dict(w_down=A[5] + 8), dict(act=None),
                 dict(y=A[7] + 2), dict(gate_up_scales=A[8]), dict(four, gate_up_scales=None), dict(four, down_scales=None),
+                dict(four, gate_up_scales=A[8] + 8), dict(four, down_scales=A[9] + 1),
                 dict(four, hidden=72, x_ld=72), dict(four, inter=40)):
         assert tokens(ep, **bad) == INV, bad
     for bad in (dict(num_tokens=65), dict(num_experts=1025, logits_ld=1025), dict(top_k=33, num_experts=64, logits_ld=64),
