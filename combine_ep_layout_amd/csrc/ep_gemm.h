@@ -13,6 +13,8 @@
 #include <stdint.h>
 #include <utility>
 
+#include "ep_wave.h"
+
 namespace epk {
 namespace {
 
@@ -23,7 +25,6 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) char lds_char;
 
-constexpr int kWave = 64;
 // Offset past every buffer's range, also with a tile's own offset added: such a
 // lane loads zeros.
 constexpr uint32_t kOutOfRange = 0x80000000u;
@@ -37,8 +38,6 @@ __device__ __forceinline__ void each_of(F&& f, std::integer_sequence<int, I...>)
 }
 template <int N, class F>
 __device__ __forceinline__ void each(F&& f) { each_of(f, std::make_integer_sequence<int, N>{}); }
-
-__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // 1 KiB from memory to LDS: lane l's 16 bytes at base + voff to lds + 16 l.
 // Not visible to the compiler's wait counting: the pipeline waits by itself.

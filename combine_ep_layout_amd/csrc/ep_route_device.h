@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "ep_layout.h"
+#include "ep_wave.h"
 
 namespace epk {
 
@@ -35,7 +36,6 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t stream);
 
 namespace {
 
-constexpr int kWave = 64;
 constexpr int kRouteMaxExperts = 1024;
 constexpr int kRouteMaxTopK = 32;
 constexpr int kRouteMaxTokens = 1 << 25;    // a wave each: the grid stays below 2^32 threads

@@ -24,6 +24,7 @@
 #include <stdint.h>
 
 #include "ep_act.h"
+#include "ep_gemm.h"
 #include "ep_layout.h"
 #include "ep_ranges.h"
 #include "ep_route_device.h"
@@ -32,8 +33,6 @@ namespace epk {
 namespace {
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = 8;
@@ -45,9 +44,6 @@ constexpr int kMaxExperts = kRouteMaxExperts;
 constexpr int kMaxUsed = kMaxExperts + kMaxSlots / 16;
 constexpr int kMaxWidth = 1 << 16;          // hidden, inter
 constexpr int64_t kMaxMatrix = 1 << 29;     // hidden * inter of one expert
-// An offset past every buffer, also with a row's own offset added: such a lane loads zeros.
-constexpr uint32_t kOutOfRange = 0x80000000u;
-
 struct TokensArgs {
     const __bf16* x;            // [T, x_ld]
     int64_t x_ld;
@@ -65,8 +61,6 @@ struct TokensArgs {
     __bf16* y;                  // [T, H]
 };
 
-__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
-
 typedef __amdgpu_buffer_rsrc_t Buffer;
 __device__ __forceinline__ Buffer buffer(const void* base, int64_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (int)(uint32_t)bytes, 0x00020000);
@@ -82,7 +76,9 @@ __device__ __forceinline__ u32x4 load16(Buffer b, uint32_t lane, int at) {
 // loaded of the tokens, which beside 4-bit weights is as many bytes as the
 // weights (64 tokens: 267 us, 338 with one); beside bf16 weights it is little, and
 // two workgroups of a compute unit that hide each other's ends are worth more
-// (24 experts of 2056 x 1000: 38 us, 43).  kUpWaves: waves of a SIMD so.
+// (24 experts of 2056 x 1000: 38 us, 43).  kUpWaves: waves of a SIMD so.  With two
+// tiles a wave a workgroup may take four, half of its waves two of them: longer
+// shares, fewer ends (launch()).
 struct Bf16Weights {
     static constexpr int kStep = 64, kFrags = 2, kUpTiles = 1, kUpWaves = 4;
     struct Regs { u32x4 v[2]; };
@@ -310,37 +306,63 @@ __device__ __forceinline__ void find_slots(const TokensArgs& a, Slots& s) {
     }
 }
 
-// What a wave loads for one step: M parts of matrices and NT tiles of 16 tokens.
-template <class W, int M, int NT>
-struct Stage {
-    typename W::Regs w[M];
-    u32x4 x[NT][W::kFrags];
-};
+// Bytes of LDS of a wave's tokens: a step of NT tiles of 16 rows.
+template <class W, int NT>
+constexpr int kTokenBytes = NT * kRows * W::kStep * 2;
 
 // A wave's stream of steps: the next one's loads follow each step's products, a
 // group's scales are loaded a group ahead.  One step ahead keeps enough bytes on
 // their way (16 waves of 4 KiB a compute unit); more of them cost (one token in
 // bf16: 131 us, 142 with four steps; 64 tokens in 4 bits: 426 us, 444).
+// The tokens' values go through LDS: loaded in the instruction's own layout, each
+// lane's 16 bytes lie in a line of their own, and the vector cache takes a lane a
+// cycle; so it takes four (64 tokens in 4 bits: 366 us, 418).
 template <class W, int M, int NT>
 struct Stream {
-    Stage<W, M, NT> stage;
+    // The tokens' pieces of 16 bytes: of a row, and rows that a load of 1 KiB covers.
+    static constexpr int kPieces = W::kStep / 8, kEach = kWave / kPieces, kLoads = kRows / kEach;
+    typename W::Regs w[M];
     typename W::Scales scales[M], ahead[M];
+    uint32_t x_at[NT][kLoads];      // the lane's piece of a load's rows, or kOutOfRange
+    i32x4 x;
+    int n;                          // rows with a token
+    lds_char* lds;
 
-    // x_at: the lane's token's offset in bytes, or kOutOfRange.  left <= 0: nothing (every lane out of range).
-    __device__ __forceinline__ void load(const typename W::Matrix (&m)[M], const typename W::Lane (&l)[M], Buffer x,
-                                         const uint32_t (&x_at)[NT], int step, int left, int q) {
-        Stage<W, M, NT>& s = stage;
-        // The buffers' range is checked less the common offset, which therefore stays inside.
-        step = left > 0 ? step : 0;
-#pragma unroll
-        for (int i = 0; i < M; ++i) s.w[i] = W::load(m[i], l[i], step, left, q);
+    // row(i): offset in bytes of the i-th token
+    template <class F>
+    __device__ __forceinline__ void set_tokens(const void* base, int count, int lane, F row) {
+        x = make_rsrc(base);
+        n = count;
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int f = 0; f < W::kFrags; ++f)
-                s.x[j][f] = load16(x, W::k_of(q, f) < left ? x_at[j] + W::k_of(q, f) * 2 : kOutOfRange, step * (W::kStep * 2));
+            for (int k = 0; k < kLoads; ++k) {
+                const int i = j * kRows + k * kEach + lane / kPieces;
+                x_at[j][k] = i < n ? row(i) + piece(lane + k * kWave) * 16 : kOutOfRange;
+            }
+    }
+    // which piece of a row a lane loads: those of eight rows that are read together lie in different banks
+    __device__ __forceinline__ static int piece(int lane) { return (lane % kPieces) ^ (lane / kPieces & 7); }
+    // left: summed indices from this step on; <= 0: nothing (every lane out of range)
+    __device__ __forceinline__ void load(const typename W::Matrix (&m)[M], const typename W::Lane (&l)[M], int step, int left, int lane) {
+        // The buffers' range is checked less the common offset, which therefore stays inside.
+        step = left > 0 ? step : 0;
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");          // the last step's tokens are read
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k) {
+                if (j * kRows + k * kEach >= n) continue;           // what is there belongs to no token
+                const bool in = piece(lane + k * kWave) * 8 < left;
+                load_to_lds(uni((int)(uint32_t)(uintptr_t)lds + (j * kLoads + k) * 1024),
+                            in && x_at[j][k] != kOutOfRange ? x_at[j][k] + (uint32_t)step * (W::kStep * 2) : kOutOfRange, x);
+            }
+#pragma unroll
+        for (int i = 0; i < M; ++i) w[i] = W::load(m[i], l[i], step, left, lane >> 4);
         __builtin_amdgcn_sched_barrier(0);
     }
+    // No load into LDS outlives the workgroup.
+    __device__ __forceinline__ static void end() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
     __device__ __forceinline__ void load_scales(const typename W::Matrix (&m)[M], const typename W::Lane (&l)[M], int step, int n) {
 #pragma unroll
         for (int i = 0; i < M; ++i) ahead[i] = W::load_scales(m[i], l[i], step, n);
@@ -353,19 +375,26 @@ struct Stream {
             W::settle(scales[i]);
         }
     }
-    __device__ __forceinline__ void multiply(int d, const typename W::Lane (&l)[M], int left, int q, f32x4 (&c)[M][NT]) const {
-        const Stage<W, M, NT>& s = stage;
+    __device__ __forceinline__ void multiply(int d, const typename W::Lane (&l)[M], int left, int lane, f32x4 (&c)[M][NT]) const {
+        const int q = lane >> 4, r = lane & 15;
         float scale[M];
 #pragma unroll
         for (int i = 0; i < M; ++i) scale[i] = W::scale_of(scales[i], l[i], d, left, q);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");            // the step's tokens are in LDS
+        bf16x8 v[NT][W::kFrags];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int f = 0; f < W::kFrags; ++f)
+                v[j][f] = *(__attribute__((address_space(3))) bf16x8*)(lds + (j * kRows + r) * (W::kStep * 2) +
+                                                                       ((W::k_of(q, f) / 8) ^ (r & 7)) * 16);
 #pragma unroll
         for (int f = 0; f < W::kFrags; ++f)
 #pragma unroll
             for (int i = 0; i < M; ++i) {
-                const bf16x8 w = W::fragment(s.w[i], scale[i], f);
+                const bf16x8 u = W::fragment(w[i], scale[i], f);
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    c[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, s.x[j][f]), c[i][j], 0, 0, 0);
+                for (int j = 0; j < NT; ++j) c[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u, v[j][f], c[i][j], 0, 0, 0);
             }
     }
 };
@@ -376,13 +405,11 @@ struct UpItem {
 };
 
 // A wave's share of an item: an eighth of the summed index.
-template <class W, int R, int NT>
+template <class W, int R, int NT, int GROUPS>
 struct UpShare {
-    static constexpr int M = 2 * R;
+    static constexpr int M = 2 * R, kParts = kWaves / GROUPS;
     typename W::Matrix m[M];
     typename W::Lane l[M];
-    uint32_t x_at[NT];
-    Buffer x;
     int begin, end, H;
     Stream<W, M, NT> stream;
 
@@ -396,24 +423,18 @@ struct UpShare {
 #pragma unroll
         for (int i = 0; i < M; ++i) {
             m[i] = i & 1 ? up : gate;
-            l[i] = W::lane(t.r0 + (i >> 1) * kRows + (lane & 15), a.I, a.H, q);
+            l[i] = W::lane(t.r0 + (wave / kParts * R + (i >> 1)) * kRows + (lane & 15), a.I, a.H, q);
         }
-        x = buffer(a.x, ((int64_t)(a.T - 1) * a.x_ld + a.H) * 2);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const int i = j * 16 + (lane & 15);
-            x_at[j] = i < t.n ? (uint32_t)(s.sorted[t.first + i] / a.K) * (uint32_t)a.x_ld * 2u : kOutOfRange;
-        }
+        stream.set_tokens(a.x, t.n, lane, [&](int i) { return (uint32_t)(s.sorted[t.first + i] / a.K) * (uint32_t)a.x_ld * 2u; });
         H = a.H;
         const int steps = (H + W::kStep - 1) / W::kStep;
-        begin = steps * wave / kWaves;
-        end = steps * (wave + 1) / kWaves;
+        begin = steps * (wave % kParts) / kParts;
+        end = steps * (wave % kParts + 1) / kParts;
         if (begin == end) return;
         stream.load_scales(m, l, begin, H);
-        stream.load(m, l, x, x_at, begin, left(begin), q);
+        stream.load(m, l, begin, left(begin), lane);
     }
     __device__ __forceinline__ void run(int lane, f32x4 (&c)[M][NT]) {
-        const int q = lane >> 4;
 #pragma unroll
         for (int i = 0; i < M; ++i)
 #pragma unroll
@@ -421,18 +442,19 @@ struct UpShare {
 #pragma unroll 1
         for (int i = begin; i < end; i += 4) {
             stream.next_group();
-            stream.load_scales(m, l, i + 4 < end ? i + 4 : i, H);
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
-                stream.multiply(d, l, left(i + d), q, c);
-                stream.load(m, l, x, x_at, i + d + 1, left(i + d + 1), q);
+                stream.multiply(d, l, left(i + d), lane, c);
+                if (d == 0) stream.load_scales(m, l, i + 4 < end ? i + 4 : i, H);
+                stream.load(m, l, i + d + 1, left(i + d + 1), lane);
             }
         }
+        stream.end();
     }
 };
 
 // The waves' sums, the activation and the store of an item.
-template <int R, int NT>
+template <int R, int NT, int GROUPS>
 __device__ __forceinline__ void up_finish(const TokensArgs& a, const Slots& s, float* red, const UpItem& t, int wave, int lane,
                                           const f32x4 (&c)[2 * R][NT]) {
     const int tid = threadIdx.x;
@@ -446,45 +468,53 @@ __device__ __forceinline__ void up_finish(const TokensArgs& a, const Slots& s, f
             to[0] = c[2 * k][j];
             to[64] = c[2 * k + 1][j];
             __syncthreads();
-            if (tid < 256) {
+            if (tid < 256 * GROUPS) {
+                constexpr int kParts = kWaves / GROUPS;
+                const int group = tid >> 8, at = tid & 255;
                 float g = 0.f, u = 0.f;
 #pragma unroll
-                for (int w = 0; w < kWaves; ++w) {
-                    g += red[w * 512 + tid];
-                    u += red[w * 512 + 256 + tid];
+                for (int w = 0; w < kParts; ++w) {
+                    g += red[(group * kParts + w) * 512 + at];
+                    u += red[(group * kParts + w) * 512 + 256 + at];
                 }
-                const int i = j * 16 + ((tid >> 2) & 15), r = t.r0 + k * kRows + (tid >> 6) * 4 + (tid & 3);
+                const int i = j * 16 + ((at >> 2) & 15), r = t.r0 + (group * R + k) * kRows + (at >> 6) * 4 + (at & 3);
                 if (i < t.n && r < a.I) a.a[(int64_t)s.sorted[t.first + i] * a.I + r] = (__bf16)(act_value(g, a.act) * u);
             }
             __syncthreads();
         }
 }
 
-template <class W, int R, int NT>
-__device__ __forceinline__ void up_item(const TokensArgs& a, const Slots& s, float* red, const UpItem& t) {
+template <class W, int R, int NT, int GROUPS>
+__device__ __forceinline__ void up_item(const TokensArgs& a, const Slots& s, float* red, lds_char* tokens, const UpItem& t) {
     const int lane = threadIdx.x & (kWave - 1), wave = uni(threadIdx.x / kWave);
-    UpShare<W, R, NT> share;
+    UpShare<W, R, NT, GROUPS> share;
     f32x4 c[2 * R][NT];
+    share.stream.lds = tokens + wave * kTokenBytes<W, NT>;
     share.start(a, s, t, wave, lane);
     share.run(lane, c);
-    up_finish<R, NT>(a, s, red, t, wave, lane, c);
+    up_finish<R, NT, GROUPS>(a, s, red, t, wave, lane, c);
 }
+
+template <class W, bool MANY>
+constexpr size_t kUpLds = kWaves * kTokenBytes<W, MANY ? 2 : 1> + kWaves * 512 * sizeof(float) + sizeof(Slots);
 
 // MANY: an expert may have more than 16 tokens.  Two tiles of them are the most
 // that the registers hold; a third and fourth are another pass over the weights.
-template <class W, int R, bool MANY, bool ROUTE>
+template <class W, int R, int GROUPS, bool MANY, bool ROUTE>
 __global__ void __launch_bounds__(kThreads, W::kUpWaves) tokens_up_kernel(TokensArgs a) {
-    __shared__ Slots s;
-    __shared__ __attribute__((aligned(16))) float red[kWaves * 512];
+    extern __shared__ __attribute__((aligned(1024))) char smem[];
+    lds_char* const tokens = (lds_char*)smem;
+    float* const red = (float*)(smem + kWaves * kTokenBytes<W, MANY ? 2 : 1>);
+    Slots& s = *(Slots*)(red + kWaves * 512);
     find_slots<ROUTE, kMaxTokens>(a, s);
-    constexpr int kSide = R * kRows;
+    constexpr int kSide = GROUPS * R * kRows;
     const int tiles = (a.I + kSide - 1) / kSide, items = uni(s.n_used) * tiles;
     for (int i = blockIdx.x; i < items; i += gridDim.x) {
         const int u = i / tiles, first = uni(s.start[u]);
         const UpItem t{uni(s.used[u]), first, uni(s.start[u + 1]) - first, (i - u * tiles) * kSide};
-        if (!MANY || t.n <= 16) up_item<W, R, 1>(a, s, red, t);
+        if (!MANY || t.n <= 16) up_item<W, R, 1, GROUPS>(a, s, red, tokens, t);
         else
-            for (int k = 0; k < t.n; k += 32) up_item<W, R, 2>(a, s, red, {t.e, first + k, t.n - k < 32 ? t.n - k : 32, t.r0});
+            for (int k = 0; k < t.n; k += 32) up_item<W, R, 2, GROUPS>(a, s, red, tokens, {t.e, first + k, t.n - k < 32 ? t.n - k : 32, t.r0});
     }
 }
 
@@ -492,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, W::kUpWaves) tokens_up_kernel(Tokens
 // groups, one after another; sums: [wave][token][columns].  An expert's further
 // tokens past 16 read its rows again, out of the L2 where they just were.
 template <class W, int R, int TOKENS>
-__device__ __forceinline__ void down_item(const TokensArgs& a, const Slots& s, float (&sums)[kWaves][TOKENS][R * kRows], int c0) {
+__device__ __forceinline__ void down_item(const TokensArgs& a, const Slots& s, float (&sums)[kWaves][TOKENS][R * kRows], lds_char* tokens, int c0) {
     constexpr int M = R, kSide = M * kRows;
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = uni(tid / kWave), q = lane >> 4;
     const int groups = (a.I + 4 * W::kStep - 1) / (4 * W::kStep), units = uni(s.n_used) * groups;
@@ -500,26 +530,24 @@ __device__ __forceinline__ void down_item(const TokensArgs& a, const Slots& s, f
     typename W::Lane l[M];
 #pragma unroll
     for (int i = 0; i < M; ++i) l[i] = W::lane(c0 + i * kRows + (lane & 15), a.H, a.I, q);
-    const Buffer x = buffer(a.a, (int64_t)a.T * a.K * a.I * 2);
     Stream<W, M, 1> stream;
+    stream.lds = tokens + wave * kTokenBytes<W, 1>;
     f32x4 c[M][1];
 #pragma unroll
     for (int i = 0; i < M; ++i) c[i][0] = f32x4{0.f, 0.f, 0.f, 0.f};
     typename W::Matrix m[M] = {};
-    uint32_t x_at[1];
     auto open = [&](int u) {
         const int e = uni(s.used[u]), first = uni(s.start[u]), n = uni(s.start[u + 1]) - first;
         const typename W::Matrix w = W::open(a.w_down, a.s_down, e, a.H, 0, a.H, a.I);
 #pragma unroll
         for (int i = 0; i < M; ++i) m[i] = w;
-        const int k = lane & 15;
-        x_at[0] = k < n ? (uint32_t)s.sorted[first + k] * (uint32_t)a.I * 2u : kOutOfRange;
+        stream.set_tokens(a.a, n, lane, [&](int i) { return (uint32_t)s.sorted[first + i] * (uint32_t)a.I * 2u; });
     };
     if (begin < end) {
         int u = begin / groups, g = begin - u * groups;         // where the products are
         open(u);
         stream.load_scales(m, l, g * 4, a.I);
-        stream.load(m, l, x, x_at, g * 4, a.I - g * 4 * W::kStep, q);
+        stream.load(m, l, g * 4, a.I - g * 4 * W::kStep, lane);
 #pragma unroll 1
         for (int i = begin; i < end; ++i) {
             // the next group: of this expert, or of the next one
@@ -528,13 +556,13 @@ __device__ __forceinline__ void down_item(const TokensArgs& a, const Slots& s, f
             stream.next_group();
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
-                stream.multiply(d, l, a.I - (g * 4 + d) * W::kStep, q, c);
+                stream.multiply(d, l, a.I - (g * 4 + d) * W::kStep, lane, c);
                 if (d < 3) {
-                    stream.load(m, l, x, x_at, g * 4 + d + 1, a.I - (g * 4 + d + 1) * W::kStep, q);
+                    stream.load(m, l, g * 4 + d + 1, a.I - (g * 4 + d + 1) * W::kStep, lane);
                 } else {
                     if (more && next_g == 0) open(u + 1);
                     stream.load_scales(m, l, more ? next_g * 4 : 0, a.I);
-                    stream.load(m, l, x, x_at, next_g * 4, more ? a.I - next_g * 4 * W::kStep : 0, q);
+                    stream.load(m, l, next_g * 4, more ? a.I - next_g * 4 * W::kStep : 0, lane);
                 }
             }
             if (next_g == 0 || !more) {
@@ -558,6 +586,7 @@ __device__ __forceinline__ void down_item(const TokensArgs& a, const Slots& s, f
             }
             g = next_g;
         }
+        stream.end();
     }
     __syncthreads();
     for (int i = tid; i < a.T * kSide; i += kThreads) {
@@ -574,19 +603,19 @@ __device__ __forceinline__ void down_item(const TokensArgs& a, const Slots& s, f
 }
 
 // The sums follow the slots: past 64 KiB together with many tokens.
-template <int R, int TOKENS>
-constexpr size_t kDownLds = sizeof(Slots) / 16 * 16 + 16 + sizeof(float) * kWaves * TOKENS * R * kRows;
+template <class W, int R, int TOKENS>
+constexpr size_t kDownLds = kWaves * kTokenBytes<W, 1> + sizeof(float) * kWaves * TOKENS * R * kRows + sizeof(Slots);
 
 template <class W, int R, int TOKENS>
 __global__ void __launch_bounds__(kThreads, 4 / R) tokens_down_kernel(TokensArgs a) {
-    extern __shared__ __attribute__((aligned(16))) char smem[];
+    extern __shared__ __attribute__((aligned(1024))) char smem[];
     constexpr int kSide = R * kRows;
-    Slots& s = *(Slots*)smem;
-    float (&sums)[kWaves][TOKENS][kSide] = *(float (*)[kWaves][TOKENS][kSide])(smem + sizeof(Slots) / 16 * 16 + 16);
+    float (&sums)[kWaves][TOKENS][kSide] = *(float (*)[kWaves][TOKENS][kSide])(smem + kWaves * kTokenBytes<W, 1>);
+    Slots& s = *(Slots*)(smem + kWaves * kTokenBytes<W, 1> + sizeof(sums));
     for (int i = threadIdx.x; i < kWaves * TOKENS * kSide; i += kThreads) (&sums[0][0][0])[i] = 0.f;
     find_slots<false, TOKENS == 16 ? kMaxTokens : 16>(a, s);        // of 16 tokens no expert has more
     const int tiles = (a.H + kSide - 1) / kSide;
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) down_item<W, R, TOKENS>(a, s, sums, tile * kSide);
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) down_item<W, R, TOKENS>(a, s, sums, (lds_char*)smem, tile * kSide);
 }
 
 // From so many tokens on, or past 256 experts, the choice has a launch of its own:
@@ -595,41 +624,46 @@ constexpr int kRouteHereTokens = kWaves;
 static_assert(kRouteHereTokens <= 16, "no expert has more");
 constexpr int kRouteHereExperts = 256;
 
-template <class W, int R, bool MANY>
+hipError_t launch_with(void (*kernel)(TokensArgs), const TokensArgs& a, int grid, size_t lds, hipStream_t stream) {
+    if (lds > 64 * 1024) {
+        const hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+        if (e != hipSuccess) return e;
+    }
+    kernel<<<grid, kThreads, lds, stream>>>(a);
+    return hipGetLastError();
+}
+
+template <class W, int R, int GROUPS, bool MANY>
 hipError_t launch_up(const TokensArgs& a, int64_t items, int num_cu, hipStream_t stream) {
     const int most = W::kUpWaves / 2 * num_cu;          // what the registers let run at once
     const int grid = (int)(items < most ? items : most);
-    bool here = false;
-    if constexpr (!MANY) {
-        here = a.route_here;
-        if (here) tokens_up_kernel<W, R, MANY, true><<<grid, kThreads, 0, stream>>>(a);
-    }
-    if (!here) tokens_up_kernel<W, R, MANY, false><<<grid, kThreads, 0, stream>>>(a);
-    return hipGetLastError();
+    constexpr size_t lds = kUpLds<W, MANY>;
+    if constexpr (!MANY)
+        if (a.route_here) return launch_with(tokens_up_kernel<W, R, GROUPS, MANY, true>, a, grid, lds, stream);
+    return launch_with(tokens_up_kernel<W, R, GROUPS, MANY, false>, a, grid, lds, stream);
 }
 
 template <class W, int R, int TOKENS>
 hipError_t launch_down(const TokensArgs& a, int64_t items, int num_cu, hipStream_t stream) {
     const int most = 2 / R * num_cu, grid = (int)(items < most ? items : most);
-    constexpr size_t lds = kDownLds<R, TOKENS>;
-    if (lds > 64 * 1024) {
-        const hipError_t e = hipFuncSetAttribute((const void*)tokens_down_kernel<W, R, TOKENS>,
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-        if (e != hipSuccess) return e;
-    }
-    tokens_down_kernel<W, R, TOKENS><<<grid, kThreads, lds, stream>>>(a);
-    return hipGetLastError();
+    return launch_with(tokens_down_kernel<W, R, TOKENS>, a, grid, kDownLds<W, R, TOKENS>, stream);
 }
 
-// One row tile a wave where two would leave half of the compute units without work.
+// Four row tiles a workgroup in the gate and up products where that leaves no more
+// rounds of the compute units behind than two (32 tokens in 4 bits, 2048 x 1024: 93 us,
+// 110); one row tile a wave where two would leave half of the compute units
+// without work.
 template <class W, bool MANY>
 hipError_t launch(const TokensArgs& a, int num_cu, hipStream_t stream) {
     constexpr int kTokens = MANY ? kMaxTokens : 16;
     const int64_t used = (int64_t)a.T * a.K < a.E ? (int64_t)a.T * a.K : a.E;
     auto items = [](int rows, int r) { return (int64_t)((rows + r * kRows - 1) / (r * kRows)); };
-    const bool up_more = used * items(a.I, W::kUpTiles) > num_cu / 2, down_two = items(a.H, 2) > num_cu / 2;
-    const hipError_t e = up_more ? launch_up<W, W::kUpTiles, MANY>(a, used * items(a.I, W::kUpTiles), num_cu, stream)
-                                 : launch_up<W, 1, MANY>(a, used * items(a.I, 1), num_cu, stream);
+    const bool down_two = items(a.H, 2) > num_cu / 2;
+    const int64_t more = used * items(a.I, W::kUpTiles), twice = used * items(a.I, 2 * W::kUpTiles);
+    auto rounds = [&](int64_t n) { return (n + num_cu - 1) / num_cu; };
+    const hipError_t e = W::kUpTiles > 1 && 2 * rounds(twice) <= rounds(more) ? launch_up<W, W::kUpTiles, 2, MANY>(a, twice, num_cu, stream)
+                         : more > num_cu / 2 ? launch_up<W, W::kUpTiles, 1, MANY>(a, more, num_cu, stream)
+                                             : launch_up<W, 1, 1, MANY>(a, used * items(a.I, 1), num_cu, stream);
     if (e != hipSuccess) return e;
     return down_two ? launch_down<W, 2, kTokens>(a, items(a.H, 2), num_cu, stream)
                     : launch_down<W, 1, kTokens>(a, items(a.H, 1), num_cu, stream);
