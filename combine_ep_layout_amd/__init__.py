@@ -2,10 +2,11 @@
 one MI355X (gfx950).
 
 Argument marshalling only: every step of layout, dispatch and combine, of the
-router, the experts' feed-forward and the optimiser runs in the library's HIP
-kernels (_ep_torch.so, host code, checks lists of tensors).  PyTorch provides
-device memory and streams; the library is loaded after torch so that both share
-torch's HIP runtime.  Import fails loudly when the library has not been built
+router, the experts' feed-forward (batches through the pool, a few tokens in one
+call) and the optimisers runs in the library's HIP kernels (_ep_torch.so, host
+code, checks lists of tensors).  PyTorch provides device memory and streams; the
+library is loaded after torch so that both share torch's HIP runtime.  Import
+fails loudly when the library has not been built
 (``python combine_ep_layout_amd/build.py``).
 
 The names follow the C ABI in include/ep_layout.h (ep_handle_create,
