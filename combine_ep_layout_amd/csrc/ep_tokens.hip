@@ -7,13 +7,12 @@
 // experts' matrices are the bytes that count, and every matrix that a token
 // uses is read once.
 //
-// A workgroup takes 16 rows of a matrix and shares the summed index out to its
-// eight waves, so that all of the chip's compute units read at once however few
+// A workgroup takes 16 to 64 rows of a matrix and shares the summed index out to
+// its waves, so that all of the chip's compute units read at once however few
 // the experts are.  A wave's product is a matrix instruction with 16 rows of
-// the weights on one side and up to 16 tokens of the expert on the other: the
-// weights go from memory to the registers in the instruction's own layout, a step
-// ahead, with no pass through LDS, and further tokens of the same expert cost no
-// bytes of theirs.  The waves' sums meet in LDS, in a fixed order.
+// the weights on one side and up to 16 tokens of the expert on the other, so
+// further tokens of the same expert cost no bytes of theirs.  The waves' sums meet
+// in LDS, in a fixed order.
 //
 // Weights are bf16, or 4-bit codes (e2m1) with an exponent byte for each 32 of
 // them: two codes become two bf16 values, exactly, in one instruction, so the
@@ -80,7 +79,7 @@ __device__ __forceinline__ u32x4 load16(Buffer b, uint32_t lane, int at) {
 // tiles a wave a workgroup may take four, half of its waves two of them: longer
 // shares, fewer ends (launch()).
 struct Bf16Weights {
-    static constexpr int kStep = 64, kFrags = 2, kUpTiles = 1, kUpWaves = 4;
+    static constexpr int kStep = 64, kFrags = 2, kTileBytes = 0, kUpTiles = 1, kUpWaves = 4;
     struct Regs { u32x4 v[2]; };
     struct Scales {};
     struct Matrix { Buffer w; };
@@ -91,16 +90,17 @@ struct Bf16Weights {
     // summed index of fragment f inside a step
     __device__ static int k_of(int q, int f) { return f * 32 + q * 8; }
     struct Lane { uint32_t at; };
-    __device__ static Lane lane(int row, int rows, int n, int q) {
+    // of the tile of rows from `first` on
+    __device__ static Lane lane(int first, int rows, int n, int lane) {
+        const int row = first + (lane & 15), q = lane >> 4;
         return {row < rows ? (uint32_t)row * (uint32_t)n * 2u + q * 16 : kOutOfRange};
     }
     // left: summed indices from this step on
-    __device__ static Regs load(const Matrix& m, const Lane& l, int step, int left, int q) {
-        Regs r;
+    __device__ static void load(Regs& r, const Matrix& m, const Lane& l, int step, int left, int lane, uint32_t) {
 #pragma unroll
-        for (int f = 0; f < 2; ++f) r.v[f] = load16(m.w, k_of(q, f) < left ? l.at + f * 64 : kOutOfRange, step * (kStep * 2));
-        return r;
+        for (int f = 0; f < 2; ++f) r.v[f] = load16(m.w, k_of(lane >> 4, f) < left ? l.at + f * 64 : kOutOfRange, step * (kStep * 2));
     }
+    __device__ static void take(Regs&, lds_char*, int) {}
     __device__ static Scales load_scales(const Matrix&, const Lane&, int, int) { return {}; }
     __device__ static void settle(Scales&) {}
     __device__ static float scale_of(const Scales&, const Lane&, int, int, int) { return 1.0f; }
@@ -110,24 +110,37 @@ struct Bf16Weights {
 };
 
 struct Mxfp4Weights {
-    static constexpr int kStep = 128, kFrags = 4, kUpTiles = 2, kUpWaves = 2;
+    static constexpr int kStep = 128, kFrags = 4, kTileBytes = kRows * 64, kUpTiles = 2, kUpWaves = 2;
     struct Regs { u32x4 v; };
     // a row's bytes of a group: four of each step (one for each quarter)
     struct Scales { u32x4 v; uint32_t more; int over; };
-    struct Matrix { Buffer w, s; int bytes; };
+    struct Matrix { i32x4 w; Buffer s; int bytes; };
     __device__ static Matrix open(const void* w, const uint8_t* s, int64_t e, int64_t each, int64_t first, int64_t rows, int n) {
         const int64_t at = e * each + first;
-        return {buffer((const uint8_t*)w + at * (n / 2), rows * (n / 2)), buffer(s + at * (n / 32), rows * (n / 32)),
+        return {make_rsrc((const uint8_t*)w + at * (n / 2)), buffer(s + at * (n / 32), rows * (n / 32)),
                 (int)(rows * (n / 32))};
     }
     __device__ static int k_of(int q, int f) { return q * 32 + f * 8; }
     struct Lane { uint32_t at, scale, shift; };
-    __device__ static Lane lane(int row, int rows, int n, int q) {
-        const uint32_t s = (uint32_t)row * (uint32_t)(n / 32);
-        return row < rows ? Lane{(uint32_t)row * (uint32_t)(n / 2) + q * 16, s & ~3u, s & 3u} : Lane{kOutOfRange, kOutOfRange, 0};
+    // The codes go through LDS, whole lines a load: lane l loads row l / 4 of the tile,
+    // the piece that lets eight rows be read together from different banks.
+    __device__ static int piece(int lane) { return (lane & 3) ^ (lane >> 3 & 3); }
+    __device__ static Lane lane(int first, int rows, int n, int lane) {
+        const int row = first + lane / 4, own = first + (lane & 15);
+        const uint32_t s = (uint32_t)own * (uint32_t)(n / 32);
+        Lane l{kOutOfRange, kOutOfRange, 0};
+        if (row < rows) l.at = (uint32_t)row * (uint32_t)(n / 2) + piece(lane) * 16;
+        if (own < rows) {
+            l.scale = s & ~3u;
+            l.shift = s & 3u;
+        }
+        return l;
     }
-    __device__ static Regs load(const Matrix& m, const Lane& l, int step, int left, int q) {
-        return {load16(m.w, q * 32 < left ? l.at : kOutOfRange, step * (kStep / 2))};
+    __device__ static void load(Regs&, const Matrix& m, const Lane& l, int step, int left, int lane, uint32_t lds) {
+        load_to_lds(uni((int)lds), l.at != kOutOfRange && piece(lane) * 32 < left ? l.at + (uint32_t)step * (kStep / 2) : kOutOfRange, m.w);
+    }
+    __device__ static void take(Regs& r, lds_char* tile, int lane) {
+        r.v = *(__attribute__((address_space(3))) u32x4*)(tile + (lane & 15) * 64 + ((lane >> 4) ^ (lane >> 1 & 3)) * 16);
     }
     // 16 bytes from the row's dword on, for rows that start inside a dword 4 more.
     // A matrix has a multiple of 32 bytes; its last row's last load comes from
@@ -306,22 +319,25 @@ __device__ __forceinline__ void find_slots(const TokensArgs& a, Slots& s) {
     }
 }
 
-// Bytes of LDS of a wave's tokens: a step of NT tiles of 16 rows.
-template <class W, int NT>
-constexpr int kTokenBytes = NT * kRows * W::kStep * 2;
+// Bytes of LDS of a wave: a step of M tiles of weights (in 4 bits) and NT tiles of tokens.
+template <class W, int M, int NT>
+constexpr int kStepBytes = M * W::kTileBytes + NT * kRows * W::kStep * 2;
 
-// A wave's stream of steps: the next one's loads follow each step's products, a
-// group's scales are loaded a group ahead.  One step ahead keeps enough bytes on
-// their way (16 waves of 4 KiB a compute unit); more of them cost (one token in
-// bf16: 131 us, 142 with four steps; 64 tokens in 4 bits: 426 us, 444).
-// The tokens' values go through LDS: loaded in the instruction's own layout, each
-// lane's 16 bytes lie in a line of their own, and the vector cache takes a lane a
-// cycle; so it takes four (64 tokens in 4 bits: 366 us, 418).
+// A wave's stream of steps, one loaded ahead; a group's scales are loaded a group
+// ahead.  More steps ahead cost (one token in bf16: 131 us, 142 with four; 64
+// tokens in 4 bits: gate and up 245 us with two, 246).
+// In the instruction's own layout each lane's 16 bytes lie in a line of their own,
+// and the vector cache's address unit takes a lane a cycle, or four lanes that
+// read 64 bytes together.  Beside 4-bit weights it was busy 84 % of the time.  So the
+// tokens' values go through LDS, loaded in whole lines (64 tokens in 4 bits:
+// gate and up 264 -> 243 us, down 160 -> 137), and the codes, too (223 and 130).
+// bf16 weights stay in registers: their LDS would leave one workgroup a compute unit.
 template <class W, int M, int NT>
 struct Stream {
     // The tokens' pieces of 16 bytes: of a row, and rows that a load of 1 KiB covers.
     static constexpr int kPieces = W::kStep / 8, kEach = kWave / kPieces, kLoads = kRows / kEach;
     typename W::Regs w[M];
+    bf16x8 v[NT][W::kFrags];
     typename W::Scales scales[M], ahead[M];
     uint32_t x_at[NT][kLoads];      // the lane's piece of a load's rows, or kOutOfRange
     i32x4 x;
@@ -347,18 +363,19 @@ struct Stream {
     __device__ __forceinline__ void load(const typename W::Matrix (&m)[M], const typename W::Lane (&l)[M], int step, int left, int lane) {
         // The buffers' range is checked less the common offset, which therefore stays inside.
         step = left > 0 ? step : 0;
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");          // the last step's tokens are read
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");          // what is there is read
+        const uint32_t at = (uint32_t)(uintptr_t)lds;
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int k = 0; k < kLoads; ++k) {
                 if (j * kRows + k * kEach >= n) continue;           // what is there belongs to no token
                 const bool in = piece(lane + k * kWave) * 8 < left;
-                load_to_lds(uni((int)(uint32_t)(uintptr_t)lds + (j * kLoads + k) * 1024),
+                load_to_lds(uni((int)at + M * W::kTileBytes + (j * kLoads + k) * 1024),
                             in && x_at[j][k] != kOutOfRange ? x_at[j][k] + (uint32_t)step * (W::kStep * 2) : kOutOfRange, x);
             }
 #pragma unroll
-        for (int i = 0; i < M; ++i) w[i] = W::load(m[i], l[i], step, left, lane >> 4);
+        for (int i = 0; i < M; ++i) W::load(w[i], m[i], l[i], step, left, lane, at + i * W::kTileBytes);
         __builtin_amdgcn_sched_barrier(0);
     }
     // No load into LDS outlives the workgroup.
@@ -375,19 +392,23 @@ struct Stream {
             W::settle(scales[i]);
         }
     }
-    __device__ __forceinline__ void multiply(int d, const typename W::Lane (&l)[M], int left, int lane, f32x4 (&c)[M][NT]) const {
+    // The step in LDS to registers.
+    __device__ __forceinline__ void take(int lane) {
         const int q = lane >> 4, r = lane & 15;
-        float scale[M];
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
-        for (int i = 0; i < M; ++i) scale[i] = W::scale_of(scales[i], l[i], d, left, q);
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");            // the step's tokens are in LDS
-        bf16x8 v[NT][W::kFrags];
+        for (int i = 0; i < M; ++i) W::take(w[i], lds + i * W::kTileBytes, lane);
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int f = 0; f < W::kFrags; ++f)
-                v[j][f] = *(__attribute__((address_space(3))) bf16x8*)(lds + (j * kRows + r) * (W::kStep * 2) +
+                v[j][f] = *(__attribute__((address_space(3))) bf16x8*)(lds + M * W::kTileBytes + (j * kRows + r) * (W::kStep * 2) +
                                                                        ((W::k_of(q, f) / 8) ^ (r & 7)) * 16);
+    }
+    __device__ __forceinline__ void multiply(int d, const typename W::Lane (&l)[M], int left, int lane, f32x4 (&c)[M][NT]) const {
+        float scale[M];
+#pragma unroll
+        for (int i = 0; i < M; ++i) scale[i] = W::scale_of(scales[i], l[i], d, left, lane >> 4);
 #pragma unroll
         for (int f = 0; f < W::kFrags; ++f)
 #pragma unroll
@@ -396,6 +417,15 @@ struct Stream {
 #pragma unroll
                 for (int j = 0; j < NT; ++j) c[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u, v[j][f], c[i][j], 0, 0, 0);
             }
+    }
+    // A step's products, and next()'s loads: those into LDS before the products, those
+    // into the registers that these are made of behind them.
+    template <class F>
+    __device__ __forceinline__ void step(int d, const typename W::Lane (&l)[M], int left, int lane, f32x4 (&c)[M][NT], F next) {
+        take(lane);
+        if constexpr (W::kTileBytes > 0) next();
+        multiply(d, l, left, lane, c);
+        if constexpr (W::kTileBytes == 0) next();
     }
 };
 
@@ -417,13 +447,12 @@ struct UpShare {
 
     // Puts the first steps' loads on their way.
     __device__ __forceinline__ void start(const TokensArgs& a, const Slots& s, const UpItem& t, int wave, int lane) {
-        const int q = lane >> 4;
         const typename W::Matrix gate = W::open(a.w_gate_up, a.s_gate_up, t.e, 2 * (int64_t)a.I, 0, a.I, a.H);
         const typename W::Matrix up = W::open(a.w_gate_up, a.s_gate_up, t.e, 2 * (int64_t)a.I, a.I, a.I, a.H);
 #pragma unroll
         for (int i = 0; i < M; ++i) {
             m[i] = i & 1 ? up : gate;
-            l[i] = W::lane(t.r0 + (wave / kParts * R + (i >> 1)) * kRows + (lane & 15), a.I, a.H, q);
+            l[i] = W::lane(t.r0 + (wave / kParts * R + (i >> 1)) * kRows, a.I, a.H, lane);
         }
         stream.set_tokens(a.x, t.n, lane, [&](int i) { return (uint32_t)(s.sorted[t.first + i] / a.K) * (uint32_t)a.x_ld * 2u; });
         H = a.H;
@@ -444,9 +473,10 @@ struct UpShare {
             stream.next_group();
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
-                stream.multiply(d, l, left(i + d), lane, c);
-                if (d == 0) stream.load_scales(m, l, i + 4 < end ? i + 4 : i, H);
-                stream.load(m, l, i + d + 1, left(i + d + 1), lane);
+                stream.step(d, l, left(i + d), lane, c, [&] {
+                    if (d == 0) stream.load_scales(m, l, i + 4 < end ? i + 4 : i, H);
+                    stream.load(m, l, i + d + 1, left(i + d + 1), lane);
+                });
             }
         }
         stream.end();
@@ -489,14 +519,14 @@ __device__ __forceinline__ void up_item(const TokensArgs& a, const Slots& s, flo
     const int lane = threadIdx.x & (kWave - 1), wave = uni(threadIdx.x / kWave);
     UpShare<W, R, NT, GROUPS> share;
     f32x4 c[2 * R][NT];
-    share.stream.lds = tokens + wave * kTokenBytes<W, NT>;
+    share.stream.lds = tokens + wave * kStepBytes<W, 2 * R, NT>;
     share.start(a, s, t, wave, lane);
     share.run(lane, c);
     up_finish<R, NT, GROUPS>(a, s, red, t, wave, lane, c);
 }
 
-template <class W, bool MANY>
-constexpr size_t kUpLds = kWaves * kTokenBytes<W, MANY ? 2 : 1> + kWaves * 512 * sizeof(float) + sizeof(Slots);
+template <class W, int R, bool MANY>
+constexpr size_t kUpLds = kWaves * kStepBytes<W, 2 * R, MANY ? 2 : 1> + kWaves * 512 * sizeof(float) + sizeof(Slots);
 
 // MANY: an expert may have more than 16 tokens.  Two tiles of them are the most
 // that the registers hold; a third and fourth are another pass over the weights.
@@ -504,7 +534,7 @@ template <class W, int R, int GROUPS, bool MANY, bool ROUTE>
 __global__ void __launch_bounds__(kThreads, W::kUpWaves) tokens_up_kernel(TokensArgs a) {
     extern __shared__ __attribute__((aligned(1024))) char smem[];
     lds_char* const tokens = (lds_char*)smem;
-    float* const red = (float*)(smem + kWaves * kTokenBytes<W, MANY ? 2 : 1>);
+    float* const red = (float*)(smem + kWaves * kStepBytes<W, 2 * R, MANY ? 2 : 1>);
     Slots& s = *(Slots*)(red + kWaves * 512);
     find_slots<ROUTE, kMaxTokens>(a, s);
     constexpr int kSide = GROUPS * R * kRows;
@@ -529,9 +559,9 @@ __device__ __forceinline__ void down_item(const TokensArgs& a, const Slots& s, f
     const int begin = (int)((int64_t)units * wave / kWaves), end = (int)((int64_t)units * (wave + 1) / kWaves);
     typename W::Lane l[M];
 #pragma unroll
-    for (int i = 0; i < M; ++i) l[i] = W::lane(c0 + i * kRows + (lane & 15), a.H, a.I, q);
+    for (int i = 0; i < M; ++i) l[i] = W::lane(c0 + i * kRows, a.H, a.I, lane);
     Stream<W, M, 1> stream;
-    stream.lds = tokens + wave * kTokenBytes<W, 1>;
+    stream.lds = tokens + wave * kStepBytes<W, R, 1>;
     f32x4 c[M][1];
 #pragma unroll
     for (int i = 0; i < M; ++i) c[i][0] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -556,14 +586,15 @@ __device__ __forceinline__ void down_item(const TokensArgs& a, const Slots& s, f
             stream.next_group();
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
-                stream.multiply(d, l, a.I - (g * 4 + d) * W::kStep, lane, c);
-                if (d < 3) {
-                    stream.load(m, l, g * 4 + d + 1, a.I - (g * 4 + d + 1) * W::kStep, lane);
-                } else {
-                    if (more && next_g == 0) open(u + 1);
-                    stream.load_scales(m, l, more ? next_g * 4 : 0, a.I);
-                    stream.load(m, l, next_g * 4, more ? a.I - next_g * 4 * W::kStep : 0, lane);
-                }
+                stream.step(d, l, a.I - (g * 4 + d) * W::kStep, lane, c, [&] {
+                    if (d < 3) {
+                        stream.load(m, l, g * 4 + d + 1, a.I - (g * 4 + d + 1) * W::kStep, lane);
+                    } else {
+                        if (more && next_g == 0) open(u + 1);
+                        stream.load_scales(m, l, more ? next_g * 4 : 0, a.I);
+                        stream.load(m, l, next_g * 4, more ? a.I - next_g * 4 * W::kStep : 0, lane);
+                    }
+                });
             }
             if (next_g == 0 || !more) {
                 // the expert's part is done: every token has it once
@@ -604,14 +635,14 @@ __device__ __forceinline__ void down_item(const TokensArgs& a, const Slots& s, f
 
 // The sums follow the slots: past 64 KiB together with many tokens.
 template <class W, int R, int TOKENS>
-constexpr size_t kDownLds = kWaves * kTokenBytes<W, 1> + sizeof(float) * kWaves * TOKENS * R * kRows + sizeof(Slots);
+constexpr size_t kDownLds = kWaves * kStepBytes<W, R, 1> + sizeof(float) * kWaves * TOKENS * R * kRows + sizeof(Slots);
 
 template <class W, int R, int TOKENS>
 __global__ void __launch_bounds__(kThreads, 4 / R) tokens_down_kernel(TokensArgs a) {
     extern __shared__ __attribute__((aligned(1024))) char smem[];
     constexpr int kSide = R * kRows;
-    float (&sums)[kWaves][TOKENS][kSide] = *(float (*)[kWaves][TOKENS][kSide])(smem + kWaves * kTokenBytes<W, 1>);
-    Slots& s = *(Slots*)(smem + kWaves * kTokenBytes<W, 1> + sizeof(sums));
+    float (&sums)[kWaves][TOKENS][kSide] = *(float (*)[kWaves][TOKENS][kSide])(smem + kWaves * kStepBytes<W, R, 1>);
+    Slots& s = *(Slots*)(smem + kWaves * kStepBytes<W, R, 1> + sizeof(sums));
     for (int i = threadIdx.x; i < kWaves * TOKENS * kSide; i += kThreads) (&sums[0][0][0])[i] = 0.f;
     find_slots<false, TOKENS == 16 ? kMaxTokens : 16>(a, s);        // of 16 tokens no expert has more
     const int tiles = (a.H + kSide - 1) / kSide;
@@ -637,7 +668,7 @@ template <class W, int R, int GROUPS, bool MANY>
 hipError_t launch_up(const TokensArgs& a, int64_t items, int num_cu, hipStream_t stream) {
     const int most = W::kUpWaves / 2 * num_cu;          // what the registers let run at once
     const int grid = (int)(items < most ? items : most);
-    constexpr size_t lds = kUpLds<W, MANY>;
+    constexpr size_t lds = kUpLds<W, R, MANY>;
     if constexpr (!MANY)
         if (a.route_here) return launch_with(tokens_up_kernel<W, R, GROUPS, MANY, true>, a, grid, lds, stream);
     return launch_with(tokens_up_kernel<W, R, GROUPS, MANY, false>, a, grid, lds, stream);
@@ -661,9 +692,17 @@ hipError_t launch(const TokensArgs& a, int num_cu, hipStream_t stream) {
     const bool down_two = items(a.H, 2) > num_cu / 2;
     const int64_t more = used * items(a.I, W::kUpTiles), twice = used * items(a.I, 2 * W::kUpTiles);
     auto rounds = [&](int64_t n) { return (n + num_cu - 1) / num_cu; };
-    const hipError_t e = W::kUpTiles > 1 && 2 * rounds(twice) <= rounds(more) ? launch_up<W, W::kUpTiles, 2, MANY>(a, twice, num_cu, stream)
-                         : more > num_cu / 2 ? launch_up<W, W::kUpTiles, 1, MANY>(a, more, num_cu, stream)
-                                             : launch_up<W, 1, 1, MANY>(a, used * items(a.I, 1), num_cu, stream);
+    hipError_t e = hipSuccess;
+    if (more <= num_cu / 2) {
+        e = launch_up<W, 1, 1, MANY>(a, used * items(a.I, 1), num_cu, stream);
+    } else {
+        bool wide = false;
+        if constexpr (W::kUpTiles > 1) {
+            wide = 2 * rounds(twice) <= rounds(more);
+            if (wide) e = launch_up<W, W::kUpTiles, 2, MANY>(a, twice, num_cu, stream);
+        }
+        if (!wide) e = launch_up<W, W::kUpTiles, 1, MANY>(a, more, num_cu, stream);
+    }
     if (e != hipSuccess) return e;
     return down_two ? launch_down<W, 2, kTokens>(a, items(a.H, 2), num_cu, stream)
                     : launch_down<W, 1, kTokens>(a, items(a.H, 1), num_cu, stream);
