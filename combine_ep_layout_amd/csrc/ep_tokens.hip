@@ -326,11 +326,11 @@ constexpr int kStepBytes = M * W::kTileBytes + NT * kRows * W::kStep * 2;
 // A wave's stream of steps, one loaded ahead; a group's scales are loaded a group
 // ahead.  More steps ahead cost (one token in bf16: 131 us, 142 with four; 64
 // tokens in 4 bits: gate and up 245 us with two, 246).
-// In the instruction's own layout each lane's 16 bytes lie in a line of their own,
-// and the vector cache's address unit takes a lane a cycle, or four lanes that
-// read 64 bytes together.  Beside 4-bit weights it was busy 84 % of the time.  So the
-// tokens' values go through LDS, loaded in whole lines (64 tokens in 4 bits:
-// gate and up 264 -> 243 us, down 160 -> 137), and the codes, too (223 and 130).
+// In the instruction's own layout each lane's 16 bytes lie in a line of their own.
+// The tokens' values, as many bytes as 4-bit weights have, go through LDS instead,
+// loaded in whole lines (64 tokens in 4 bits: gate and up 264 -> 243 us, down
+// 160 -> 137), and the codes, too (223 and 130; the vector cache's address unit
+// busy for 102 M cycles instead of 116 M in gate and up).
 // bf16 weights stay in registers: their LDS would leave one workgroup a compute unit.
 template <class W, int M, int NT>
 struct Stream {
