@@ -324,8 +324,8 @@ template <class W, int M, int NT>
 constexpr int kStepBytes = M * W::kTileBytes + NT * kRows * W::kStep * 2;
 
 // A wave's stream of steps, one loaded ahead; a group's scales are loaded a group
-// ahead.  More steps ahead cost (one token in bf16: 131 us, 142 with four; 64
-// tokens in 4 bits: gate and up 245 us with two, 246).
+// ahead.  More steps ahead cost (one token in bf16: 131 us, 142 with four) or bring
+// nothing (64 tokens in 4 bits, gate and up: 246 us, 245 with two).
 // In the instruction's own layout each lane's 16 bytes lie in a line of their own.
 // The tokens' values, as many bytes as 4-bit weights have, go through LDS instead,
 // loaded in whole lines (64 tokens in 4 bits: gate and up 264 -> 243 us, down
