@@ -27,6 +27,7 @@
 #include "ep_layout.h"
 #include "ep_ranges.h"
 #include "ep_route_device.h"
+#include "ep_tokens_shape.h"
 
 namespace epk {
 namespace {
@@ -34,9 +35,9 @@ namespace {
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kWaves = 8;
+constexpr int kWaves = kTokensWaves;
 constexpr int kThreads = kWaves * kWave;
-constexpr int kRows = 16;                   // rows of a matrix that a workgroup takes
+constexpr int kRows = kTokensRows;
 constexpr int kMaxTokens = 64;
 constexpr int kMaxSlots = kMaxTokens * kRouteMaxTopK;
 constexpr int kMaxExperts = kRouteMaxExperts;
@@ -649,12 +650,6 @@ __global__ void __launch_bounds__(kThreads, 4 / R) tokens_down_kernel(TokensArgs
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) down_item<W, R, TOKENS>(a, s, sums, (lds_char*)smem, tile * kSide);
 }
 
-// From so many tokens on, or past 256 experts, the choice has a launch of its own:
-// a workgroup would have to make more than its waves can at once.
-constexpr int kRouteHereTokens = kWaves;
-static_assert(kRouteHereTokens <= 16, "no expert has more");
-constexpr int kRouteHereExperts = 256;
-
 hipError_t launch_with(void (*kernel)(TokensArgs), const TokensArgs& a, int grid, size_t lds, hipStream_t stream) {
     if (lds > 64 * 1024) {
         const hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
@@ -680,37 +675,30 @@ hipError_t launch_down(const TokensArgs& a, int64_t items, int num_cu, hipStream
     return launch_with(tokens_down_kernel<W, R, TOKENS>, a, grid, kDownLds<W, R, TOKENS>, stream);
 }
 
-// Four row tiles a workgroup in the gate and up products where that leaves no more
-// rounds of the compute units behind than two (32 tokens in 4 bits, 2048 x 1024: 93 us,
-// 110); one row tile a wave where two would leave half of the compute units
-// without work.
 template <class W, bool MANY>
-hipError_t launch(const TokensArgs& a, int num_cu, hipStream_t stream) {
+hipError_t launch(const TokensArgs& a, const TokensShape& f, int num_cu, hipStream_t stream) {
     constexpr int kTokens = MANY ? kMaxTokens : 16;
-    const int64_t used = (int64_t)a.T * a.K < a.E ? (int64_t)a.T * a.K : a.E;
-    auto items = [](int rows, int r) { return (int64_t)((rows + r * kRows - 1) / (r * kRows)); };
-    const bool down_two = items(a.H, 2) > num_cu / 2;
-    const int64_t more = used * items(a.I, W::kUpTiles), twice = used * items(a.I, 2 * W::kUpTiles);
-    auto rounds = [&](int64_t n) { return (n + num_cu - 1) / num_cu; };
     hipError_t e = hipSuccess;
-    if (more <= num_cu / 2) {
-        e = launch_up<W, 1, 1, MANY>(a, used * items(a.I, 1), num_cu, stream);
-    } else {
-        bool wide = false;
-        if constexpr (W::kUpTiles > 1) {
-            wide = 2 * rounds(twice) <= rounds(more);
-            if (wide) e = launch_up<W, W::kUpTiles, 2, MANY>(a, twice, num_cu, stream);
-        }
-        if (!wide) e = launch_up<W, W::kUpTiles, 1, MANY>(a, more, num_cu, stream);
+    if (f.up_tiles == 1) {
+        e = launch_up<W, 1, 1, MANY>(a, f.up_items, num_cu, stream);
+    } else if constexpr (W::kUpTiles > 1) {
+        e = f.up_groups == 2 ? launch_up<W, W::kUpTiles, 2, MANY>(a, f.up_items, num_cu, stream)
+                             : launch_up<W, W::kUpTiles, 1, MANY>(a, f.up_items, num_cu, stream);
     }
     if (e != hipSuccess) return e;
-    return down_two ? launch_down<W, 2, kTokens>(a, items(a.H, 2), num_cu, stream)
-                    : launch_down<W, 1, kTokens>(a, items(a.H, 1), num_cu, stream);
+    return f.down_tiles == 2 ? launch_down<W, 2, kTokens>(a, f.down_items, num_cu, stream)
+                             : launch_down<W, 1, kTokens>(a, f.down_items, num_cu, stream);
 }
 
 template <class W>
-hipError_t launch(const TokensArgs& a, int num_cu, hipStream_t stream) {
-    return a.T <= 16 ? launch<W, false>(a, num_cu, stream) : launch<W, true>(a, num_cu, stream);
+hipError_t launch(TokensArgs& a, int num_cu, hipStream_t stream) {
+    const TokensShape f = tokens_shape({a.T, a.K, a.E, a.H, a.I, W::kUpTiles, num_cu});
+    a.route_here = a.route.logits && f.route_here;
+    if (a.route.logits && !a.route_here) {
+        const hipError_t e = launch_route(a.route, stream);
+        if (e != hipSuccess) return e;
+    }
+    return f.many ? launch<W, true>(a, f, num_cu, stream) : launch<W, false>(a, f, num_cu, stream);
 }
 
 constexpr uint32_t kRouteFlags = EP_ROUTE_BF16 | EP_ROUTE_SIGMOID | EP_ROUTE_NORMALIZE;
@@ -785,8 +773,6 @@ extern "C" ep_status ep_moe_tokens(const ep_moe_tokens_args* p, hipStream_t stre
         a.route.bias = p->bias;
         a.route.idx = p->topk_idx;
         a.route.weights = p->topk_weights;
-        a.route_here = T <= kRouteHereTokens && E <= kRouteHereExperts;
-        if (!a.route_here && launch_route(a.route, stream) != hipSuccess) return EP_ERR_HIP;
     }
     const hipError_t e = four ? launch<Mxfp4Weights>(a, num_cu, stream) : launch<Bf16Weights>(a, num_cu, stream);
     return e == hipSuccess ? EP_OK : EP_ERR_HIP;
