@@ -35,6 +35,7 @@
 
 #include "ep_gemm.h"
 #include "ep_layout.h"
+#include "ep_muon_shape.h"
 #include "ep_ranges.h"
 
 namespace epk {
@@ -42,12 +43,7 @@ namespace {
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
-// The products: G, P, the next X, and the last X into the results (of tall
-// matrices through LDS, which turns it).
-enum Op { kGram, kPoly, kNext, kLast, kLastTall };
-constexpr bool is_update(int op) { return op >= kNext; }
-
-constexpr int kProblems = 40;               // shapes of a launch: the arguments stay below 4 KiB
+constexpr int kProblems = kMuonProblems;
 constexpr int kMaxSide = 1 << 16;
 constexpr int64_t kMaxMatrix = 1 << 29;     // values: a matrix of fp16 stays below 2 GiB
 constexpr int kGroupM = 8;                  // row tiles that share their column tiles' loads
@@ -322,13 +318,6 @@ struct Shape {
     static constexpr int kLoads = A::kLoads + B::kLoads;
     static constexpr size_t kLds = (size_t)ST * kStageBytes;
 };
-
-// Tiles of one matrix.
-template <int BM, int BN>
-__host__ __device__ inline int64_t tiles_of(int op, int m, int ld_n) {
-    const int64_t down = (m + BM - 1) / BM;
-    return is_update(op) ? down * ((ld_n + BN - 1) / BN) : down * (down + 1) / 2;
-}
 
 // The eight sums of a lane out of two fragments, consecutive along the side that
 // its sums lie on; lane l's first is at eight_at(l) of the fragments' places.
@@ -621,53 +610,28 @@ hipError_t launch_shape(GroupArgs& a, const Place& at) {
     return hipGetLastError();
 }
 
-// Rounds of wide tiles that so many middle ones cost, two on a compute unit (8
-// matrices of 2048 x 7168, G: 183 us a wide round, 119 one of 512 middle tiles).
-double middle_cost(int64_t tiles, int num_cu) {
-    const int64_t rest = tiles % (2 * num_cu);
-    return 0.65 * (double)(tiles / (2 * num_cu)) + (rest == 0 ? 0.0 : rest <= num_cu ? 0.42 : 0.65);
-}
-
-// The tiles of a product.  Wide ones are the fastest where they come in whole
-// rounds of the compute units; what is left of a last round goes to the middle
-// ones, by whole matrices (8 matrices, G: 252 wide and 136 middle tiles instead of
-// two rounds of 288).  Less than 5/8 of a compute unit's worth of middle tiles:
-// small ones (16 matrices of 256 x 512, the next X: 8.4 us, 13.0).
 template <int OP>
 hipError_t launch_product(GroupArgs& a, const Place& at) {
-    const int64_t wide = set_tiles<Wide<OP>>(a), middle = set_tiles<Middle<OP>>(a), cu = at.num_cu;
-    if (middle < cu * 5 / 8) return launch_shape<Small<OP>>(a, at);
-    const double all_wide = (double)((wide + cu - 1) / cu), all_middle = middle_cost(middle, (int)cu);
-    GroupArgs rest = a;
-    double best = all_wide < all_middle ? all_wide : all_middle;
-    bool mixed = false;
-    if (wide > cu && wide % cu != 0) {
-        // the fewest matrices from the end on that leave whole rounds
-        GroupArgs front = a;
-        rest.count = 0;
-        int64_t over = wide % cu, less = 0, more = 0;
-        for (int i = a.count - 1; i >= 0 && less < over; --i) {
-            const Problem& p = a.p[i];
-            const int64_t each = tiles_of<256, 256>(OP, p.m, p.ld_n);
-            int64_t k = (over - less + each - 1) / each;
-            k = k < p.mats ? k : p.mats;
-            Problem& q = rest.p[rest.count++] = p;
-            q.begin = p.begin + p.mats - (int)k;
-            q.mats = (int)k;
-            front.p[i].mats = p.mats - (int)k;
-            if (front.p[i].mats == 0) front.count = i;
-            less += k * each;
-            more += k * tiles_of<128, 128>(OP, p.m, p.ld_n);
+    MuonSizes sizes[kProblems];
+    for (int i = 0; i < a.count; ++i) sizes[i] = {a.p[i].m, a.p[i].ld_n, a.p[i].mats};
+    const MuonShape f = muon_shape(OP, a.count, sizes, at.num_cu);
+    if (f.small) return launch_shape<Small<OP>>(a, at);
+    GroupArgs part = a;
+    auto take = [&](bool wide) {
+        part.count = 0;
+        for (int i = 0; i < a.count; ++i) {
+            const int mats = wide ? f.wide_mats[i] : a.p[i].mats - f.wide_mats[i];
+            if (mats == 0) continue;
+            Problem& q = part.p[part.count++] = a.p[i];
+            q.begin += wide ? 0 : f.wide_mats[i];
+            q.mats = mats;
         }
-        const double cost = (double)((wide - less + cu - 1) / cu) + middle_cost(more, (int)cu);
-        if (front.count > 0 && cost < best - 0.05) {            // another launch costs something, too
-            mixed = true;
-            const hipError_t e = launch_shape<Wide<OP>>(front, at);
-            if (e != hipSuccess) return e;
-        }
-    }
-    if (mixed) return launch_shape<Middle<OP>>(rest, at);
-    return all_wide < all_middle ? launch_shape<Wide<OP>>(a, at) : launch_shape<Middle<OP>>(a, at);
+    };
+    take(true);
+    const hipError_t e = launch_shape<Wide<OP>>(part, at);
+    if (e != hipSuccess) return e;
+    take(false);
+    return launch_shape<Middle<OP>>(part, at);
 }
 
 // The last products of the wide or of the tall problems.
@@ -764,25 +728,22 @@ struct Runner {
     GroupArgs a{};
     char* ws;
     int64_t bytes, used = 0;
-    int64_t tiles = 0;
+    int64_t blocks = 0;         // of a launch, at most
     int steps;
     Place at;
 
     hipError_t flush() {
         hipError_t e = a.count ? run_group(a, steps, at) : hipSuccess;
         a.count = 0;
-        used = tiles = 0;
+        used = blocks = 0;
         return e;
     }
     // size of param and copy in bytes a value, x as the flags say
     hipError_t add(Problem p, int64_t batch, int64_t x_size, int64_t param_size) {
         const int64_t each = p.ws_each(), n = (int64_t)p.m * p.n;
-        // a launch's tiles stay far below 2^31
-        const int64_t tiles_each = tiles_of<64, 64>(kNext, p.m, p.ld_n) + p.partials, most_tiles = (int64_t)1 << 28;
+        const int64_t blocks_each = muon_blocks_of(p.m, p.ld_n, p.partials);
         for (int64_t done = 0; done < batch;) {
-            int64_t fit = (bytes - used) / each;
-            const int64_t fit_tiles = (most_tiles - tiles) / tiles_each;
-            fit = fit < fit_tiles ? fit : fit_tiles;
+            const int64_t fit = muon_fit(bytes - used, each, blocks, blocks_each);
             if (a.count == kProblems || fit < 1) {
                 const hipError_t e = flush();
                 if (e != hipSuccess) return e;
@@ -798,7 +759,7 @@ struct Runner {
             if (p.copy) q.copy = p.copy + done * n;
             q.ws = ws + used;
             used += k * each;
-            tiles += k * tiles_each;
+            blocks += k * blocks_each;
             done += k;
         }
         return hipSuccess;
