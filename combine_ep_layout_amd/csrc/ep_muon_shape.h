@@ -14,7 +14,8 @@ enum MuonOp { kGram, kPoly, kNext, kLast, kLastTall };
 constexpr bool is_update(int op) { return op >= kNext; }
 
 constexpr int kMuonProblems = 40;           // shapes of a launch: its arguments stay below 4 KiB
-constexpr int64_t kMuonMostBlocks = (int64_t)1 << 28;      // workgroups of a launch
+// Workgroups of a launch: 2^31 threads of at most 2^32 - 1.
+constexpr int64_t kMuonMostBlocks = (int64_t)1 << 23;
 
 // Tiles of one matrix.
 template <int BM, int BN>

@@ -620,8 +620,9 @@ ep_status ep_adamw(const ep_adamw_tensor* tensors, int32_t count, const ep_adamw
  * above do with room to spare; past that results are not finite.  A matrix
  * of zeros has X = 0; one with an infinity or NaN has a result that is none, and
  * spoils no other.  Sums are made in a fixed order.
- * 2 launches and up to 6 a step for up to 40 tensors as the workspace holds them
- * (up to 2 more with both tall and other matrices); capturable. */
+ * 2 launches and up to 6 a step for up to 40 tensors (and 2.7 million matrices)
+ * as the workspace holds them, up to 2 more with both tall and other matrices;
+ * capturable. */
 #define EP_MUON_PARAM_BF16 (1u << 19)
 #define EP_MUON_GRAD_BF16  (1u << 20)
 #define EP_MUON_NESTEROV   (1u << 21)

@@ -89,3 +89,21 @@ def test_what_lies_around_stays(shape):
     assert torch.equal(out, want)
     assert bool((room[:256] == 0xFF).all()) and bool((room[-256:] == 0xFF).all())
     assert bool((out_room[:32] == 7).all()) and bool((out_room[-32:] == 7).all())
+
+
+def test_millions_of_tiny_matrices():
+    """More than one launch holds, in a list and in one tensor."""
+    import combine_ep_layout_amd as ep
+    n = 1 << 20
+    base = ref.matrices("noise", 64, 1, 1, dev(), 8)
+    x = base.repeat(n // 64, 1, 1)
+    want = in_fp32(base, 5)
+    ref.check("X", want, base, rounding=2.0 ** -24)
+    params = [torch.zeros(n, 1, 1, device=dev()) for _ in range(9)]
+    ep.muon(params, [x.clone() for _ in params], [torch.zeros_like(x) for _ in params], lr=-1.0, momentum=0.0,
+            weight_decay=0.0, nesterov=False, scale=1.0)
+    for p in params:
+        assert torch.equal(p.view(-1, 64, 1, 1), want.expand(n // 64, 64, 1, 1))
+    base = ref.matrices("noise", 64, 3, 5, dev(), 9)
+    out = ep.orthogonalize(base.repeat(n // 64, 1, 1))
+    assert torch.equal(out.view(-1, 64, 3, 5), ep.orthogonalize(base).expand(n // 64, 64, 3, 5))

@@ -36,18 +36,38 @@ int main(int n, char** v) {
 """
 
 
-@pytest.fixture(scope="module")
-def program(tmp_path_factory):
+# v: bytes of the workspace, of a matrix, m, ld_n, partial sums of a matrix.  Matrices that a launch takes, filled by tensors
+# of at most 2^20.
+FIT = r"""
+#include <cstdio>
+#include <cstdlib>
+#include "ep_muon_shape.h"
+using namespace epk;
+int main(int, char** v) {
+    const long long bytes = atoll(v[1]), each = atoll(v[2]), blocks_each = muon_blocks_of(atoi(v[3]), atoi(v[4]), atoi(v[5]));
+    long long all = 0;
+    for (int i = 0; i < kMuonProblems; ++i) {
+        const long long fit = muon_fit(bytes - all * each, each, all * blocks_each, blocks_each);
+        all += fit < 1 << 20 ? fit : 1 << 20;
+    }
+    printf("%lld\n", all);
+}
+"""
+
+
+def compiled(tmp_path_factory, text):
     d = tmp_path_factory.mktemp("shape")
-    (d / "shape.cpp").write_text(PROGRAM)
+    (d / "shape.cpp").write_text(text)
     subprocess.run(["g++", "-std=c++17", "-Wall", "-I", os.path.join(ROOT, "combine_ep_layout_amd", "csrc"), "-o",
                     str(d / "shape"), str(d / "shape.cpp")], check=True)
     return str(d / "shape")
 
 
 @pytest.fixture(scope="module")
-def tiles(program):
+def tiles(tmp_path_factory):
     """{product: [(small, middle, wide) matrices of each tensor]}."""
+    program = compiled(tmp_path_factory, PROGRAM)
+
     def f(*tensors, cu=256):
         out = subprocess.run([program, str(cu), *(str(n) for t in tensors for n in t)], check=True, capture_output=True,
                              text=True).stdout
@@ -93,3 +113,25 @@ def test_tiles(tiles, tensors, want):
 def test_one_compute_unit_and_no_matrices(tiles):
     assert tiles((1, 1, 1), cu=1)["gram"]
     assert tiles((0, 64, 64))["gram"] == [(0, 0, 0)]
+
+
+@pytest.fixture(scope="module")
+def fit(tmp_path_factory):
+    program = compiled(tmp_path_factory, FIT)
+    return lambda *v: int(subprocess.run([program, *map(str, v)], check=True, capture_output=True, text=True).stdout)
+
+
+@pytest.mark.parametrize("bytes_", [4 << 30, 250 << 30])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (2, 4), (6, 8), (1, 9000), (64, 64), (128, 128), (300, 500), (65536, 8192)])
+def test_threads_of_a_launch(fit, rows, cols, bytes_):
+    """However many tiny matrices go through at once, a launch's threads, 256 a workgroup, are counted in 32 bits."""
+    m, n = sorted((rows, cols))
+    up8 = lambda v: (v + 7) // 8 * 8
+    chunks = (m * n + 8191) // 8192
+    partials = (chunks + 1) // 2 * 2 if chunks < 256 else 256
+    each = 6 * m * up8(n) + 4 * m * up8(m) + 8 * partials
+    many = fit(bytes_, each, m, up8(n), partials)
+    assert many >= 1
+    # the partial sums' launch has a workgroup each, the split at most one for 512 pieces of 8 values
+    assert many * partials * 256 < 2 ** 32
+    assert many * ((m * up8(n) // 8 + 511) // 512) * 256 < 2 ** 32
