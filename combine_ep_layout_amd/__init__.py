@@ -567,7 +567,8 @@ def moe_tokens(x: torch.Tensor, w_gate_up, w_down, logits: Optional[torch.Tensor
     [num_experts, hidden, inter] in bf16, or both Mxfp4 of these shapes.  With logits
     and top_k the choice is route()'s (score, bias, normalize and scale as there);
     otherwise topk_idx int32 and topk_weights float32 [num_tokens, top_k] make it, and
-    an index outside [0, num_experts) is masked."""
+    an index outside [0, num_experts) is masked.  Where experts have more than some 20
+    tokens each, layout_dispatch and expert_ffn are faster."""
     four = isinstance(w_gate_up, tuple)
     if four != isinstance(w_down, tuple):
         raise TypeError("w_gate_up and w_down must both be bfloat16 tensors or both Mxfp4")

@@ -4,8 +4,9 @@
 //
 // Two launches: the choice of the experts with the gate and up products and the
 // activation, then the down products with the weighted sum.  No rows move: the
-// experts' matrices are the bytes that count, and every matrix that a token
-// uses is read once.
+// experts' matrices are the bytes that count.  A matrix that a token uses is read
+// once for 32 of its expert's tokens in the gate and up products, once for 16 in
+// the down product, and again for further ones.
 //
 // A workgroup takes 16 to 64 rows of a matrix and shares the summed index out to
 // its waves, so that all of the chip's compute units read at once however few
@@ -78,7 +79,7 @@ __device__ __forceinline__ u32x4 load16(Buffer b, uint32_t lane, int at) {
 // two workgroups of a compute unit that hide each other's ends are worth more
 // (24 experts of 2056 x 1000: 38 us, 43).  kUpWaves: waves of a SIMD so.  With two
 // tiles a wave a workgroup may take four, half of its waves two of them: longer
-// shares, fewer ends (launch()).
+// shares, fewer ends (ep_tokens_shape.h).
 struct Bf16Weights {
     static constexpr int kStep = 64, kFrags = 2, kTileBytes = 0, kUpTiles = 1, kUpWaves = 4;
     struct Regs { u32x4 v[2]; };
@@ -530,7 +531,8 @@ template <class W, int R, bool MANY>
 constexpr size_t kUpLds = kWaves * kStepBytes<W, 2 * R, MANY ? 2 : 1> + kWaves * 512 * sizeof(float) + sizeof(Slots);
 
 // MANY: an expert may have more than 16 tokens.  Two tiles of them are the most
-// that the registers hold; a third and fourth are another pass over the weights.
+// that the registers hold; a third and fourth are another pass over the weights
+// (the same 8 experts: 32 tokens fetch them once, 108 us, 64 twice, 192).
 template <class W, int R, int GROUPS, bool MANY, bool ROUTE>
 __global__ void __launch_bounds__(kThreads, W::kUpWaves) tokens_up_kernel(TokensArgs a) {
     extern __shared__ __attribute__((aligned(1024))) char smem[];
@@ -551,7 +553,9 @@ __global__ void __launch_bounds__(kThreads, W::kUpWaves) tokens_up_kernel(Tokens
 
 // R row tiles of columns of y from c0 on.  A wave takes an eighth of the used experts'
 // groups, one after another; sums: [wave][token][columns].  An expert's further
-// tokens past 16 read its rows again, out of the L2 where they just were.
+// tokens past 16 read its rows again, and not out of the L2: with 8 experts of
+// 7168 x 2048 (bf16) that every token chooses, 32 and 64 tokens fetch 2 and 4
+// times the bytes of 16 (95 and 167 us, 60).
 template <class W, int R, int TOKENS>
 __device__ __forceinline__ void down_item(const TokensArgs& a, const Slots& s, float (&sums)[kWaves][TOKENS][R * kRows], lds_char* tokens, int c0) {
     constexpr int M = R, kSide = M * kRows;

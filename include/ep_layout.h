@@ -476,8 +476,12 @@ ep_status ep_expert_ffn_backward(const ep_handle* h, uint32_t epoch, const void*
  * memory with anything else (EP_ERR_INVALID_ARGUMENT).  Sums are fp32 in a fixed
  * order, weights included; a and y are each rounded once.  A token's row of y
  * depends on nothing of the other tokens but the order of its sums: infinities
- * and NaN stay in their rows.  Two launches, three with logits of more than
- * 8 tokens or 256 experts; capturable. */
+ * and NaN stay in their rows.  An expert's gate and up matrices are read once for
+ * 32 of its tokens, its down matrix once for 16: where the experts have more than
+ * some 20 each, a layout and a dispatch are the better call (bf16, 7168 x 2048, 8
+ * experts that every token chooses: 16 tokens 150 us here and 188 so, 32 199 and
+ * 182, 64 351 and 198).  Two launches, three with logits of more than 8 tokens or
+ * 256 experts; capturable. */
 #define EP_MOE_MXFP4 (1u << 17)
 typedef struct ep_moe_tokens_args {
     const void* x;
@@ -513,8 +517,8 @@ ep_status ep_moe_tokens(const ep_moe_tokens_args* args, hipStream_t stream);
  * A block's byte is the least one under which none of its values is larger than
  * 6 (0 for a block of zeros); values go to the nearest code, ties to the even
  * one.  A block with an infinity or a NaN gets byte 255, which reads as NaN.
- * The cast back writes bf16; code times 2^(b - 127) is exact there but for
- * the subnormals and for 2^128 and more, which is infinity.
+ * The cast back writes bf16; code times 2^(b - 127) is exact there (2^-128 is a
+ * subnormal of it) but for 2^128 and more, which is infinity.
  * values, codes and out are 16-byte aligned; what is written shares no memory
  * with anything else (EP_ERR_INVALID_ARGUMENT).  One launch; capturable. */
 #define EP_MXFP4_BF16 (1u << 18)
